@@ -512,6 +512,218 @@ int moe_layer_forward_noalloc(const float* logits, const uint16_t* x, int64_t T,
                               const int32_t* w2_qzeros, int32_t H, int32_t I,
                               int32_t group_size, uint16_t* out, void* stream);
 
+/* ------------------------------------------------------------------------- *
+ * MXFP4: microscaled 4-bit floating point, its products and the layer on it
+ *
+ * Layout of a matrix of R rows and K columns (K a multiple of 32, <= 65536):
+ *   codes   int32 [R, K/8]   E2M1 codes; nibble j of word w is column 8w+j:
+ *                            sign, 2 exponent bits (bias 1), 1 mantissa bit:
+ *                            0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives
+ *   scales  uint8 [R, B]     B = moe_mxfp4_scale_bytes(K) = 4 ceil(K / 128);
+ *                            byte b is the E8M0 scale 2^(byte - 127) of
+ *                            columns [32b, 32b + 32), 255 stands for NaN;
+ *                            bytes from K/32 on are padding, written as 127
+ *                            and ignored when read
+ * Expert weights are [E, N, ...] of such matrices, N the output columns.
+ *
+ * Typed tensors: a dtype code says fp32, fp16 or bf16, a stride is the
+ * distance of two rows in elements (>= the columns, <= 2^31); rows are
+ * contiguous, and such a tensor's pointer needs its element's alignment only.
+ * Functions below do not change the ABI version: they are found by name.
+ * ------------------------------------------------------------------------- */
+#define MOE_F32 0
+#define MOE_F16 1
+#define MOE_BF16 2
+
+/* Bytes of one row's scales (0: K is not a valid length).  Host only. */
+int moe_mxfp4_scale_bytes(int32_t K);
+
+/*
+ * moe_mxfp4_quantize - rows to MXFP4.  Per block of 32 columns, with m the
+ * largest magnitude: e = clamp(floor(log2 m) - 2, -127, 127), scale byte
+ * e + 127, codes the nearest E2M1 values of x 2^-e, ties to even, at most 6 in
+ * size.  A zero block has scale byte 0.  A block that holds an infinity or a
+ * NaN has scale byte 255 and zero codes: it reads back as NaN.
+ * moe_mxfp4_dequantize - the values they stand for, rounded once to dtype.
+ *
+ *   x       in/out  dtype [rows, K], stride x_stride
+ *   codes   out/in  int32 [rows, K/8]
+ *   scales  out/in  uint8 [rows, moe_mxfp4_scale_bytes(K)]
+ *
+ * rows == 0 is valid (nothing is done); rows < 2^31.
+ */
+int moe_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t K,
+                       int64_t x_stride, int32_t* codes, uint8_t* scales,
+                       void* stream);
+int moe_mxfp4_dequantize(const int32_t* codes, const uint8_t* scales,
+                         int64_t rows, int32_t K, void* x, int32_t dtype,
+                         int64_t x_stride, void* stream);
+
+/*
+ * moe_mxfp4_grouped_gemm - rows times their expert's weights, both MXFP4:
+ *   out[r, n] = sum_k A[a(r), k] * W[e, n, k]
+ *                                for expert_offsets[e] <= r < expert_offsets[e+1]
+ * Products are exact, summed in fp32, rounded once to out_dtype.  a(r) = r, or
+ * row_slots[r] / top_k when row_slots is given (moe_permute's sorted_slots:
+ * the rows of the tokens, without a copy in expert order); a slot outside
+ * [0, a_rows * top_k) takes a row of zeros.  Rows outside
+ * [expert_offsets[0], expert_offsets[E]) are left as they were.  A NaN scale
+ * makes every sum that it enters NaN.
+ *
+ *   a_codes, a_scales  in   MXFP4 [a_rows, K]
+ *   row_slots          in   int32 [rows], or NULL (then rows <= a_rows)
+ *   expert_offsets     in   int32 [E + 1], ascending, or NULL with E == 1:
+ *                           every row belongs to the one expert
+ *   w_codes, w_scales  in   MXFP4 [E, N, K]
+ *   out                out  out_dtype [rows, N], stride out_stride
+ *
+ * Limits: 1 <= E <= 4096; 1 <= N <= 65536; N * K < 2^32; rows <= 2^27 and
+ * (rows / 16 + min(E, rows)) * ceil(N / 64) < 2^24.
+ */
+int moe_mxfp4_grouped_gemm(const int32_t* a_codes, const uint8_t* a_scales,
+                           int64_t a_rows, const int32_t* row_slots,
+                           int32_t top_k, int64_t rows,
+                           const int32_t* expert_offsets, int32_t E,
+                           const int32_t* w_codes, const uint8_t* w_scales,
+                           int32_t N, int32_t K, void* out, int32_t out_dtype,
+                           int64_t out_stride, void* stream);
+
+/*
+ * moe_mxfp4_gate_up - the gate/up half of an expert FFN on MXFP4 weights:
+ *   h = A[a(r), :] . W13[e]^T (2I values, fp32), a = SiLU(h[0:I]) * h[I:2I],
+ * and a, as moe_mxfp4_quantize turns fp32 rows of I columns to MXFP4, is
+ * stored: the operand of the down product (moe_mxfp4_grouped_gemm with
+ * N = H, K = I).  Arguments and rows as there, with K = H and N = 2I.
+ *
+ *   act_codes   out  int32 [rows, I/8]
+ *   act_scales  out  uint8 [rows, moe_mxfp4_scale_bytes(I)]
+ *
+ * Limits: as there; I a multiple of 32, <= 32768.
+ */
+int moe_mxfp4_gate_up(const int32_t* a_codes, const uint8_t* a_scales,
+                      int64_t a_rows, const int32_t* row_slots, int32_t top_k,
+                      int64_t rows, const int32_t* expert_offsets, int32_t E,
+                      const int32_t* w13_codes, const uint8_t* w13_scales,
+                      int32_t I, int32_t H, int32_t* act_codes,
+                      uint8_t* act_scales, void* stream);
+
+/* Workspace bytes moe_mxfp4_layer_forward needs (0: invalid sizes). */
+size_t moe_mxfp4_layer_workspace_bytes(int64_t T, int32_t top_k, int32_t E,
+                                       int32_t H, int32_t I);
+
+/*
+ * moe_mxfp4_layer_forward - moe_layer_forward on MXFP4 experts, activations
+ * quantised too: moe_route_permute, moe_mxfp4_quantize of x, moe_mxfp4_gate_up
+ * over moe_permute's sorted_slots, moe_mxfp4_grouped_gemm into fp32 rows and
+ * moe_combine_masked, in one call; out is what those calls produce, bit for
+ * bit.
+ *
+ *   logits      in   fp32 [T, E]
+ *   x, out      in, out  dtype [T, H], dense
+ *   w13_*       in   MXFP4 [E, 2I, H], rows [0, I) gate, [I, 2I) up
+ *   w2_*        in   MXFP4 [E, H, I]
+ *   workspace   scratch, device, >= moe_mxfp4_layer_workspace_bytes(...);
+ *               contents on entry are ignored.  Two calls that overlap in time
+ *               must not share it.
+ *
+ * Errors as the calls it stands for; nothing is enqueued on an error that the
+ * arguments show.
+ */
+int moe_mxfp4_layer_forward(const float* logits, const void* x, int32_t dtype,
+                            int64_t T, int32_t E, int32_t top_k,
+                            const int32_t* w13_codes, const uint8_t* w13_scales,
+                            const int32_t* w2_codes, const uint8_t* w2_scales,
+                            int32_t H, int32_t I, void* out, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- *
+ * Token rows to expert order and back, with slots left out, and gradients
+ * ------------------------------------------------------------------------- */
+
+/* Workspace bytes moe_permute_masked needs (0 up to 1024 slots). */
+size_t moe_permute_masked_workspace_bytes(int64_t T, int32_t top_k, int32_t E);
+
+/*
+ * moe_permute_masked - moe_permute for ids that may leave slots out: a slot
+ * counts when first_expert <= id < first_expert + E, as expert id -
+ * first_expert; any other id (padding tokens: -1; experts held elsewhere)
+ * drops it.  A token may name an expert more than once.  With R slots kept:
+ *
+ *   expert_offsets  out  int32 [E + 1]   offsets[0] = 0, offsets[E] = R
+ *   sorted_slots    out  int32 [S]       slot held by row r < R, by expert, then
+ *                                        ascending; -1 from R on
+ *   slot_rows       out  int32 [S]       row of slot s, -1 for a dropped one
+ *   active_experts, num_active           as moe_permute
+ *   workspace       scratch, device, >= moe_permute_masked_workspace_bytes(...)
+ *
+ * Limits: 1 <= E <= 4096; 1 <= top_k <= 64; S < 2^31; first_expert >= 0.
+ */
+int moe_permute_masked(const int32_t* topk_ids, int64_t T, int32_t top_k,
+                       int32_t first_expert, int32_t E, int32_t* expert_offsets,
+                       int32_t* sorted_slots, int32_t* slot_rows,
+                       int32_t* active_experts, int32_t* num_active,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_dispatch - token rows to expert order: x_sorted[slot_rows[s], :] =
+ * x[s / top_k, :] for every slot s whose row is in [0, rows); rows that no
+ * slot points at are left as they were.  Rows of distinct slots are distinct
+ * (moe_permute, moe_permute_masked).
+ * moe_dispatch_backward - its gradient: grad_x[t, :] = sum_j
+ * grad_sorted[slot_rows[t * top_k + j], :], j ascending, in fp32, rounded
+ * once; a token without a slot gets zeros.  Rows that no slot points at are
+ * not read.
+ *
+ *   x, grad_x              dtype [T, H], stride x_stride
+ *   x_sorted, grad_sorted  dtype [rows, H], stride sorted_stride
+ *   slot_rows              in  int32 [T * top_k]
+ *
+ * Limits: 1 <= H <= 65536 (any H); 1 <= top_k <= 64; T * top_k, rows < 2^31.
+ */
+int moe_dispatch(const void* x, int32_t dtype, int64_t T, int32_t top_k,
+                 int32_t H, int64_t x_stride, const int32_t* slot_rows,
+                 int64_t rows, void* x_sorted, int64_t sorted_stride,
+                 void* stream);
+int moe_dispatch_backward(const void* grad_sorted, int32_t dtype, int64_t T,
+                          int32_t top_k, int32_t H, int64_t sorted_stride,
+                          const int32_t* slot_rows, int64_t rows, void* grad_x,
+                          int64_t x_stride, void* stream);
+
+/*
+ * moe_combine_masked - moe_combine for typed rows and slots left out:
+ *   out[t, :] = sum_j topk_weights[t, j] * y_sorted[slot_rows[t * top_k + j], :]
+ * over the slots whose row is in [0, rows), j ascending, in fp32, rounded
+ * once; a token without one gets zeros, and a dropped slot's weight and row
+ * are not used, whatever they hold.
+ * moe_combine_backward - its gradients:
+ *   grad_y[slot_rows[s], :] = topk_weights[s] * grad_out[s / top_k, :]
+ *   grad_weights[s] = sum_h grad_out[s / top_k, h] * y_sorted[slot_rows[s], h]
+ * with 0 for a dropped slot; rows of grad_y that no slot points at are left
+ * as they were.  grad_y must not overlap y_sorted or grad_out.
+ *
+ *   y_sorted      in   y_dtype [rows, H], stride y_stride
+ *   topk_weights  in   fp32 [T, top_k]
+ *   slot_rows     in   int32 [T * top_k]
+ *   out           out  out_dtype [T, H], stride out_stride
+ *   grad_out      in   grad_dtype [T, H], stride grad_stride
+ *   grad_y        out  y_dtype [rows, H], stride grad_y_stride
+ *   grad_weights  out  fp32 [T, top_k]
+ *
+ * Limits as moe_dispatch.
+ */
+int moe_combine_masked(const void* y_sorted, int32_t y_dtype, int64_t T,
+                       int32_t top_k, int32_t H, int64_t y_stride,
+                       const float* topk_weights, const int32_t* slot_rows,
+                       int64_t rows, void* out, int32_t out_dtype,
+                       int64_t out_stride, void* stream);
+int moe_combine_backward(const void* grad_out, int32_t grad_dtype,
+                         int64_t grad_stride, const void* y_sorted,
+                         int32_t y_dtype, int64_t y_stride,
+                         const float* topk_weights, const int32_t* slot_rows,
+                         int64_t T, int32_t top_k, int32_t H, int64_t rows,
+                         void* grad_y, int64_t grad_y_stride,
+                         float* grad_weights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,3 +23,4 @@ from .moe_oracle import (  # noqa: F401
     unpack_weight_codes,
     unpack_zero_codes,
 )
+from . import mxfp4_oracle  # noqa: E402,F401

@@ -16,7 +16,9 @@ INCLUDE = os.path.join(os.path.dirname(PKG_DIR), "include")
 LIB_NAME = "libmoe_w4a16.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["abi.hip", "plan.hip", "route.hip", "permute.hip", "route_permute.hip",
-           "router_gate.hip", "ffn_decode.hip", "ffn_prefill.hip", "combine.hip"]
+           "router_gate.hip", "ffn_decode.hip", "ffn_prefill.hip", "combine.hip",
+           "abi_mxfp4.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip", "permute_masked.hip",
+           "dispatch.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -1,0 +1,158 @@
+// MXFP4 quantisation and dequantisation.  A block is 32 consecutive values of
+// a row.  With m = max |x| of the block:
+//   e     = clamp(floor(log2 m) - 2, -127, 127)      (2: E2M1's largest exponent)
+//   code  = nearest E2M1 value of x 2^-e, ties to even, at most 6 in size
+//   scale = e + 127, one byte
+// A zero block has e = -127; a block that holds an infinity or a NaN has scale
+// byte 255, which stands for NaN, and zero codes.
+//
+// Both are bound by memory: one pass, 8 values (one code word) per lane, so
+// loads and code stores of a wave are contiguous; the four lanes of a block
+// meet by DPP inside their quad.  m is the largest bit pattern with the sign
+// cleared, so an infinity or a NaN shows in the same maximum.
+#include "mxfp4.h"
+#include "mxfp4_tile.h"
+#include "typed.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // code words per lane, their loads in flight together
+constexpr int kMaxBlocks = 1 << 20;
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  const uint32_t o = __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+  return v > o ? v : o;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(
+    const typename T::bits* __restrict__ x, int64_t rows, int words, int64_t ld,
+    uint32_t* __restrict__ codes, uint8_t* __restrict__ scales, int sbytes) {
+  const int64_t total = rows * words;
+  constexpr int kPerBlock = kThreads * kUnroll;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kPerBlock; base < total;
+       base += static_cast<int64_t>(gridDim.x) * kPerBlock) {
+    const int64_t row0 = base / words;
+    const uint32_t rem0 = static_cast<uint32_t>(base - row0 * words);
+    float v[kUnroll][8];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t off = rem0 + u * kThreads + threadIdx.x;
+      const uint32_t r = off / static_cast<uint32_t>(words);
+      const int64_t row = row0 + r;
+      if (row < rows) {
+        load8<T>(x + row * ld + 8 * static_cast<int64_t>(off - r * words), 8, v[u]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t off = rem0 + u * kThreads + threadIdx.x;
+      const uint32_t r = off / static_cast<uint32_t>(words);
+      const uint32_t c = off - r * words;
+      const int64_t row = row0 + r;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m = max(m, abs_bits(v[u][i]));
+      }
+      m = quad_max<0xB1>(m);  // lanes 1 0 3 2
+      m = quad_max<0x4E>(m);  // lanes 2 3 0 1
+      const uint32_t byte = mx_scale_byte(m);
+      // 2^-e; an exact product unless it is far below the smallest code
+      const float inv = __builtin_bit_cast(float, (254u - byte) << 23);
+      uint32_t q = 0;
+      if (byte != 255) {
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[u][0] * inv, v[u][1] * inv, 1.f, 0);
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[u][2] * inv, v[u][3] * inv, 1.f, 1);
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[u][4] * inv, v[u][5] * inv, 1.f, 2);
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[u][6] * inv, v[u][7] * inv, 1.f, 3);
+      }
+      if (row < rows) {
+        codes[row * words + c] = q;
+        if ((c & 3) == 0)
+          store_scale(scales + row * sbytes, c >> 2, words >> 2, sbytes, byte);
+      }
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(
+    const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows, int words,
+    int sbytes, typename T::bits* __restrict__ x, int64_t ld) {
+  const int64_t total = rows * words;
+  constexpr int kPerBlock = kThreads * kUnroll;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kPerBlock; base < total;
+       base += static_cast<int64_t>(gridDim.x) * kPerBlock) {
+    const int64_t row0 = base / words;
+    const uint32_t rem0 = static_cast<uint32_t>(base - row0 * words);
+    uint32_t q[kUnroll], s[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t off = rem0 + u * kThreads + threadIdx.x;
+      const uint32_t r = off / static_cast<uint32_t>(words);
+      const uint32_t c = off - r * words;
+      const int64_t row = row0 + r;
+      q[u] = row < rows ? codes[row * words + c] : 0u;
+      s[u] = row < rows ? scales[row * sbytes + (c >> 2)] : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t off = rem0 + u * kThreads + threadIdx.x;
+      const uint32_t r = off / static_cast<uint32_t>(words);
+      const uint32_t c = off - r * words;
+      const int64_t row = row0 + r;
+      const auto p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], 1.f, 0);
+      const auto p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], 1.f, 1);
+      const auto p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], 1.f, 2);
+      const auto p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], 1.f, 3);
+      float v[8] = {p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+      const int e = static_cast<int>(s[u]) - 127;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = s[u] == 255u ? __builtin_nanf("") : ldexpf(v[i], e);
+      if (row < rows) store8<T>(x + row * ld + 8 * static_cast<int64_t>(c), 8, v);
+    }
+  }
+}
+
+int grid_for(int64_t rows, int words) {
+  const int64_t n = (rows * words + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+  return static_cast<int>(n < kMaxBlocks ? n : kMaxBlocks);
+}
+
+}  // namespace
+
+void launch_mx_quantize(const void* x, int dtype, int64_t rows, int K, int64_t ld, int32_t* codes,
+                        uint8_t* scales, hipStream_t stream) {
+  const int words = K / 8;
+  const dim3 grid(grid_for(rows, words));
+  with_dtype(dtype, [&](auto t) {
+    using T = decltype(t);
+    const auto* p = static_cast<const typename T::bits*>(x);
+    auto* q = reinterpret_cast<uint32_t*>(codes);
+    hipLaunchKernelGGL(quantize_kernel<T>, grid, dim3(kThreads), 0, stream, p, rows, words,
+                       ld, q, scales, mx_scale_bytes(K));
+  });
+}
+
+void launch_mx_dequantize(const int32_t* codes, const uint8_t* scales, int64_t rows, int K, void* x,
+                          int dtype, int64_t ld, hipStream_t stream) {
+  const int words = K / 8;
+  const dim3 grid(grid_for(rows, words));
+  with_dtype(dtype, [&](auto t) {
+    using T = decltype(t);
+    auto* p = static_cast<typename T::bits*>(x);
+    const auto* q = reinterpret_cast<const uint32_t*>(codes);
+    hipLaunchKernelGGL(dequantize_kernel<T>, grid, dim3(kThreads), 0, stream, q, scales,
+                       rows, words, mx_scale_bytes(K), p, ld);
+  });
+}
+
+}  // namespace moe

@@ -1,0 +1,149 @@
+// Device helpers of the MXFP4 products: scaled matrix operands, buffer loads,
+// the tile search over expert segments, and the quantising epilogue.
+#pragma once
+
+#include "mxfp4.h"
+#include "typed.h"
+
+namespace moe {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kFp4 = 4;                          // operand format code: E2M1
+constexpr uint32_t kOutOfRange = 0x80000000u;    // past every descriptor's range (< 2^31 bytes)
+constexpr int kRawBuffer = 0x00020000;           // descriptor word 3: raw access on gfx9
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0), bytes,
+                                           kRawBuffer);
+}
+__device__ __forceinline__ dwords4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  return __builtin_bit_cast(dwords4, __builtin_amdgcn_raw_buffer_load_b128(r, static_cast<int>(at), 0, 0));
+}
+__device__ __forceinline__ uint32_t buffer_load4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b32(r, static_cast<int>(at), 0, 0);
+}
+// 16 bytes at a 4-byte aligned address.
+__device__ __forceinline__ dwords4 load_words4(const void* p) {
+  struct __attribute__((packed, aligned(4), may_alias)) Words { dwords4 d; };
+  return static_cast<const Words*>(p)->d;
+}
+
+// The instruction takes eight registers for its widest formats and reads the
+// first four for 4-bit codes.
+__device__ __forceinline__ i32x8 operand(dwords4 d) {
+  return __builtin_bit_cast(i32x8, __builtin_shufflevector(d, d, 0, 1, 2, 3, -1, -1, -1, -1));
+}
+
+// Row of A that output row r takes (-1: none).
+__device__ __forceinline__ int64_t a_row(const MxGemmArgs& p, int r) {
+  if (p.row_slots == nullptr) return r;
+  const int s = p.row_slots[r];
+  if (s < 0) return -1;
+  const int t = s / p.top_k;
+  return t < p.a_rows ? t : -1;
+}
+
+// Tile `mt` of `size` rows in the sequence of all experts' tiles, experts
+// ascending: its expert and rows [r0, r1).  False behind the last tile.  The
+// whole wave searches: each lane counts the tiles of its share of experts, a
+// scan over the lanes finds the one that holds mt.  Offsets are held inside
+// [0, rows], so damaged ones cannot lead out of the tensors.
+__device__ __forceinline__ bool find_tile(const int* __restrict__ offsets, int E, int rows,
+                                          int size, int mt, int& e, int& r0, int& r1) {
+  if (offsets == nullptr) {
+    e = 0;
+    r0 = mt * size;
+    r1 = min(rows, r0 + size);
+    return r0 < rows;
+  }
+  const int lane = threadIdx.x & 63;
+  const int per = (E + 63) >> 6;
+  constexpr int kFly = 8;
+  int sum = 0;
+  for (int i0 = 0; i0 < per; i0 += kFly) {
+    int o[kFly + 1];
+#pragma unroll
+    for (int i = 0; i <= kFly; ++i) {
+      const int at = min(lane * per + min(i0 + i, per), E);
+      o[i] = min(max(offsets[at], 0), rows);
+    }
+#pragma unroll
+    for (int i = 0; i < kFly; ++i) sum += (max(o[i + 1] - o[i], 0) + size - 1) / size;
+  }
+  int inc = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(inc, d, 64);
+    if (lane >= d) inc += v;
+  }
+  const unsigned long long past = __ballot(inc > mt);
+  if (past == 0) return false;
+  const int owner = __builtin_ctzll(past);
+  int at = __builtin_amdgcn_readlane(inc - sum, owner);  // tiles before the owner's experts
+  e = owner * per;
+  for (;; ++e) {
+    const int a = min(max(offsets[e], 0), rows), b = min(max(offsets[e + 1], 0), rows);
+    const int n = (max(b - a, 0) + size - 1) / size;
+    if (mt < at + n || e + 1 >= E) {
+      r0 = a + (mt - at) * size;
+      r1 = min(b, r0 + size);
+      return r0 < r1;
+    }
+    at += n;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(typename T::bits* p, int n, f32x4 v) {
+  if (n >= 4) {
+    if constexpr (kBytes<T> == 4) {
+      store16(p, __builtin_bit_cast(dwords4, v));
+    } else {
+      typedef uint32_t dwords2 __attribute__((ext_vector_type(2)));
+      struct __attribute__((packed, aligned(2), may_alias)) Unaligned8 { dwords2 d; };
+      dwords2 d;
+      d[0] = static_cast<uint32_t>(from_float(T{}, v[0])) |
+             (static_cast<uint32_t>(from_float(T{}, v[1])) << 16);
+      d[1] = static_cast<uint32_t>(from_float(T{}, v[2])) |
+             (static_cast<uint32_t>(from_float(T{}, v[3])) << 16);
+      reinterpret_cast<Unaligned8*>(p)->d = d;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = from_float(T{}, v[i]);
+  }
+}
+
+// ---- the quantising epilogue ---------------------------------------------------
+__device__ __forceinline__ float silu_mul(float gate, float up) {
+  return gate / (1.f + expf(-gate)) * up;
+}
+__device__ __forceinline__ uint32_t abs_bits(float v) {
+  return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;
+}
+// The scale byte of a block whose largest magnitude has bits m (255: it holds
+// an infinity or a NaN).
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t m) {
+  const uint32_t field = m >> 23;
+  return field == 255 ? 255u : (field > 2 ? field - 2 : 0u);
+}
+// Codes of two values in the low byte (zero for a NaN block).
+__device__ __forceinline__ uint32_t mx_pair(float a, float b, uint32_t byte) {
+  const float inv = __builtin_bit_cast(float, (254u - byte) << 23);
+  if (byte == 255) return 0;
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, a * inv, b * inv, 1.f, 0) & 0xFFu;
+}
+// Block `blk`'s scale of a row of `blocks`; the last one also sets the row's
+// padding, which stands for 1.
+__device__ __forceinline__ void store_scale(uint8_t* row, int blk, int blocks, int sbytes,
+                                            uint32_t byte) {
+  row[blk] = static_cast<uint8_t>(byte);
+  if (blk + 1 == blocks)
+    for (int p = blocks; p < sbytes; ++p) row[p] = 127;
+}
+
+}  // namespace moe
