@@ -163,6 +163,7 @@ PRODUCTS = [  # E, rows, N, K
     (1, 1, 1, 32), (1, 1, 64, 128), (1, 17, 33, 160), (1, 300, 200, 512), (1, 129, 257, 1184),
     (3, 40, 96, 640), (8, 80, 80, 2560), (8, 1000, 130, 96), (37, 90, 48, 544), (512, 80, 64, 256),
     (64, 2500, 160, 256), (4096, 60, 32, 64), (2, 700, 320, 1024),
+    (1, 1100, 300, 1440), (3, 2000, 520, 256), (16, 300, 260, 800), (16, 700, 136, 96),
 ]
 
 
@@ -279,7 +280,8 @@ def _check_act(codes, scales, h, size, I, K):
 
 
 @pytest.mark.parametrize("E,R,I,K", [(1, 1, 32, 32), (1, 20, 96, 160), (8, 80, 160, 2560),
-                                     (5, 600, 64, 288), (512, 80, 32, 128), (2, 333, 640, 256)])
+                                     (5, 600, 64, 288), (512, 80, 32, 128), (2, 333, 640, 256),
+                                     (16, 300, 160, 160), (16, 640, 96, 480), (1, 700, 96, 160), (2, 1500, 224, 416)])
 def test_gate_up(ops, E, R, I, K):
     rng = np.random.default_rng(R + I)
     a = _random_mx(rng, R, K, low=124, high=126)

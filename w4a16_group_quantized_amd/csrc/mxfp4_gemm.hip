@@ -14,6 +14,8 @@
 #include "mxfp4_tile.h"
 #include "typed.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -37,7 +39,7 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxGemmArgs p, int n_tile
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mt = blockIdx.x / n_tiles, nt = blockIdx.x - mt * n_tiles;
   int e, r0, r1;
-  if (!find_tile(p.offsets, p.E, p.rows, kTokens, mt, e, r0, r1)) return;
+  if (!find_tile(count_tiles(p.offsets, p.E, p.rows, kTokens), mt, e, r0, r1)) return;
 
   const int blocks = p.K / 32;  // 32-value blocks per row
   const int sbytes = mx_scale_bytes(p.K);
@@ -149,9 +151,296 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxGemmArgs p, int n_tile
   }
 }
 
-}  // namespace
+// ------------------------------------------------------------------- tiles --
+// More rows per expert: a workgroup takes BW weight rows x BT tokens and walks
+// K in chunks of 256 values (128 bytes of codes and 8 of scales per row).
+// Chunks go from memory straight to LDS (no registers in between), STAGES of
+// them: chunk c + STAGES - 1 is requested while chunk c is multiplied, one
+// barrier per chunk.  In LDS a row's eight 16-byte blocks are stored with
+// their number xor (row mod 8), so the 16-byte reads of 8 neighbouring rows
+// meet different banks.  Each stage is an array of its own: the compiler then
+// knows that reading one does not wait for the loads into another.
+//
+// Rows behind a segment or behind N are loaded as they come (or not at all,
+// past the descriptors' ranges): each result depends on its own row and token
+// only, and theirs are not stored.
+template <int BW_, int BT_, int WW_, int WT_, int STAGES_>
+struct TileShape {
+  static constexpr int BW = BW_, BT = BT_, WW = WW_, WT = WT_, STAGES = STAGES_;
+  static constexpr int kWaves = WW * WT;
+  static constexpr int NW = BW / 32 / WW, NT = BT / 32 / WT;  // 32 x 32 results per wave
+  static constexpr int kCodes = (BW + BT) * 128;
+  static constexpr int kStage = kCodes + (BW + BT) * 8;
+  static constexpr int kLoadW = BW / 8 / kWaves, kLoadT = BT / 8 / kWaves;
+  static constexpr int kScaleW = (BW / 32 + kWaves - 1) / kWaves;
+  static constexpr int kScaleT = (BT / 32 + kWaves - 1) / kWaves;
+  static constexpr int kLoads = kLoadW + kLoadT + kScaleW + kScaleT;  // per wave and chunk
+  static_assert(kLoadW * kWaves * 8 == BW && kLoadT * kWaves * 8 == BT, "loads divide evenly");
+};
 
-void launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
+typedef __attribute__((address_space(3))) void lds_void;
+
+// 16 or 4 bytes per lane, from the lane's offset to consecutive places from dst on.
+__device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t at) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, static_cast<int>(at), 0, 0, 0);
+}
+__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t at) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, static_cast<int>(at), 0, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads_and_barrier() {
+  // all but the N newest loads done, LDS reads done, then the barrier; nothing
+  // that touches memory moves across
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <typename S, bool GATE_UP, typename TO>
+__global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, int n_tiles) {
+  __shared__ __attribute__((aligned(16))) uint8_t st0[S::kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t st1[S::kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t st2[S::STAGES > 2 ? S::kStage : 16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ww = wave / S::WT, wt = wave % S::WT;
+
+  // Tiles in groups of kGroup token tiles, tokens fastest, and each XCD (the
+  // workgroups of equal index mod 8) a contiguous run of them: the tiles that
+  // run together share weight rows and tokens in its L2.
+  constexpr int kGroupTiles = 4;
+  const Tiles tiles = count_tiles(p.offsets, p.E, p.rows, S::BT);
+  const int all = tiles.total * n_tiles;
+  const int run = (all + 7) >> 3;
+  const int q = blockIdx.x >> 3;
+  const int tile = (blockIdx.x & 7) * run + q;
+  if (q >= run || tile >= all) return;
+  const int grp = tile / (kGroupTiles * n_tiles);
+  const int in = tile - grp * kGroupTiles * n_tiles;
+  const int gm = min(kGroupTiles, tiles.total - grp * kGroupTiles);
+  const int nt = in / gm;
+  int e, r0, r1;
+  if (!find_tile(tiles, grp * kGroupTiles + in - nt * gm, e, r0, r1)) return;
+
+  const int blocks = p.K / 32;
+  const int row_bytes = p.K / 2, sbytes = mx_scale_bytes(p.K);
+  const int I = p.N / 2;
+  // Weight row of tile row rr: gate/up alternates 32 gate and 32 up rows.
+  auto w_row = [&](int rr) {
+    if constexpr (GATE_UP)
+      return ((rr >> 5) & 1) * I + nt * (S::BW / 2) + (rr >> 6) * 32 + (rr & 31);
+    else
+      return nt * S::BW + rr;
+  };
+  const auto rw = make_rsrc(p.w_codes + static_cast<int64_t>(e) * p.N * row_bytes,
+                            static_cast<uint32_t>(p.N) * row_bytes);
+  const auto rws = make_rsrc(p.w_scales + static_cast<int64_t>(e) * p.N * sbytes,
+                             static_cast<uint32_t>(p.N) * sbytes);
+  const int64_t first = p.row_slots == nullptr ? r0 : 0;
+  auto clip = [](int64_t n) {
+    return static_cast<uint32_t>(n < INT32_MAX ? n : INT32_MAX);
+  };
+  const auto ra = make_rsrc(p.a_codes + first * row_bytes, clip((p.a_rows - first) * row_bytes));
+  const auto ras = make_rsrc(p.a_scales + first * sbytes, clip((p.a_rows - first) * sbytes));
+  auto t_row = [&](int tr) -> uint32_t {  // row of A, relative to `first`
+    if (p.row_slots == nullptr) return tr;
+    const int64_t a = r0 + tr < r1 ? a_row(p, r0 + tr) : -1;
+    return a < 0 ? 0u : static_cast<uint32_t>(a);
+  };
+
+  uint32_t at_w[S::kLoadW], at_t[S::kLoadT], at_ws[S::kScaleW], at_ts[S::kScaleT];
+  // the 32 rows whose scales this wave loads; spare waves repeat a load
+  auto scale_set = [&](int i, int sets) { return (i * S::kWaves + wave) % sets; };
+#pragma unroll
+  for (int i = 0; i < S::kLoadW; ++i) {
+    const int rr = (i * S::kWaves + wave) * 8 + (lane >> 3);
+    at_w[i] = static_cast<uint32_t>(w_row(rr)) * row_bytes + ((lane ^ rr) & 7) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < S::kLoadT; ++i) {
+    const int tr = (i * S::kWaves + wave) * 8 + (lane >> 3);
+    at_t[i] = t_row(tr) * row_bytes + ((lane ^ tr) & 7) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < S::kScaleW; ++i)
+    at_ws[i] = static_cast<uint32_t>(w_row(scale_set(i, S::BW / 32) * 32 + (lane >> 1))) * sbytes +
+               (lane & 1) * 4;
+#pragma unroll
+  for (int i = 0; i < S::kScaleT; ++i)
+    at_ts[i] = t_row(scale_set(i, S::BT / 32) * 32 + (lane >> 1)) * sbytes + (lane & 1) * 4;
+
+  auto load = [&](uint8_t* st, int c) {
+#pragma unroll
+    for (int i = 0; i < S::kLoadW; ++i)
+      load16_to_lds(rw, st + (i * S::kWaves + wave) * 1024, at_w[i] + c * 128);
+#pragma unroll
+    for (int i = 0; i < S::kLoadT; ++i)
+      load16_to_lds(ra, st + S::BW * 128 + (i * S::kWaves + wave) * 1024, at_t[i] + c * 128);
+#pragma unroll
+    for (int i = 0; i < S::kScaleW; ++i)
+      load4_to_lds(rws, st + S::kCodes + scale_set(i, S::BW / 32) * 256, at_ws[i] + c * 8);
+#pragma unroll
+    for (int i = 0; i < S::kScaleT; ++i)
+      load4_to_lds(ras, st + S::kCodes + S::BW * 8 + scale_set(i, S::BT / 32) * 256, at_ts[i] + c * 8);
+  };
+
+  const int col = lane & 31, g = lane >> 5;
+  f32x16 acc[S::NW][S::NT] = {};
+  // Step s multiplies blocks 2s and 2s + 1 of the chunk, lane half g taking
+  // block 2s + g; its scale byte is byte 2s + g of the row's eight.
+  auto compute = [&](const uint8_t* st) {
+    auto frag = [&](int row, int s) {
+      return *reinterpret_cast<const dwords4*>(st + row * 128 + (((2 * s + g) ^ row) & 7) * 16);
+    };
+    auto scale = [&](int row) {
+      uint2 v = *reinterpret_cast<const uint2*>(st + S::kCodes + row * 8);
+      v.x >>= 8 * g;
+      v.y >>= 8 * g;
+      return v;
+    };
+    uint2 ws[S::NW], ts[S::NT];
+#pragma unroll
+    for (int i = 0; i < S::NW; ++i) ws[i] = scale((ww * S::NW + i) * 32 + col);
+#pragma unroll
+    for (int i = 0; i < S::NT; ++i) ts[i] = scale(S::BW + (wt * S::NT + i) * 32 + col);
+    auto step = [&](auto sc) {
+      constexpr int s = decltype(sc)::value;
+      dwords4 w[S::NW], t[S::NT];
+#pragma unroll
+      for (int i = 0; i < S::NW; ++i) w[i] = frag((ww * S::NW + i) * 32 + col, s);
+#pragma unroll
+      for (int i = 0; i < S::NT; ++i) t[i] = frag(S::BW + (wt * S::NT + i) * 32 + col, s);
+#pragma unroll
+      for (int i = 0; i < S::NW; ++i)
+#pragma unroll
+        for (int j = 0; j < S::NT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              operand(w[i]), operand(t[j]), acc[i][j], kFp4, kFp4, 2 * (s & 1),
+              s < 2 ? ws[i].x : ws[i].y, 2 * (s & 1), s < 2 ? ts[j].x : ts[j].y);
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+  };
+  // A last chunk of fewer than 8 blocks: the others become zeros of scale 1.
+  auto cut = [&](uint8_t* st, int live) {
+    for (int i = threadIdx.x; i < (S::BW + S::BT) * 8; i += 64 * S::kWaves) {
+      const int row = i >> 3, b = i & 7;
+      if (b < live) continue;
+      *reinterpret_cast<dwords4*>(st + row * 128 + ((b ^ row) & 7) * 16) = dwords4{};
+      st[S::kCodes + row * 8 + b] = 127;
+    }
+  };
+
+  const int chunks = (blocks + 7) / 8;
+  auto stage = [&](uint8_t* cur, uint8_t* next, int c) {
+    // the newest STAGES - 2 chunks may still be on their way, near the end fewer
+    if (c + S::STAGES - 2 < chunks)
+      wait_loads_and_barrier<(S::STAGES - 2) * S::kLoads>();
+    else
+      wait_loads_and_barrier<0>();
+    if (blocks - 8 * c < 8) {
+      cut(cur, blocks - 8 * c);
+      wait_loads_and_barrier<0>();
+    }
+    if (c + S::STAGES - 1 < chunks) load(next, c + S::STAGES - 1);
+    compute(cur);
+  };
+  load(st0, 0);
+  if constexpr (S::STAGES == 2) {
+    for (int c = 0; c < chunks; c += 2) {
+      stage(st0, st1, c);
+      if (c + 1 < chunks) stage(st1, st0, c + 1);
+    }
+  } else {
+    if (chunks > 1) load(st1, 1);
+    for (int c = 0; c < chunks; c += 3) {
+      stage(st0, st2, c);
+      if (c + 1 < chunks) stage(st1, st0, c + 1);
+      if (c + 2 < chunks) stage(st2, st1, c + 2);
+    }
+  }
+
+  // acc[i][j][4 q + r] is weight row 32 i' + 8 q + 4 g + r of token 32 j' + col
+#pragma unroll
+  for (int j = 0; j < S::NT; ++j) {
+    const int row = r0 + (wt * S::NT + j) * 32 + col;
+    if (row >= r1) continue;  // both lane halves of a token alike
+    const bool none = p.row_slots != nullptr && a_row(p, row) < 0;
+    if constexpr (!GATE_UP) {
+      auto* o = static_cast<typename TO::bits*>(p.out) + row * p.out_ld;
+#pragma unroll
+      for (int i = 0; i < S::NW; ++i)
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          const int n0 = nt * S::BW + (ww * S::NW + i) * 32 + 8 * q4 + 4 * g;
+          f32x4 v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = none ? 0.f : acc[i][j][4 * q4 + r];
+          store4<TO>(o + n0, p.N - n0, v);
+        }
+    } else {
+      const int sb = mx_scale_bytes(I);
+#pragma unroll
+      for (int i = 0; i < S::NW; i += 2) {
+        const int blk = nt * (S::BW / 64) + (ww * S::NW + i) / 2;
+        float a[16];
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          a[r] = none ? 0.f : silu_mul(acc[i][j][r], acc[i + 1][j][r]);
+          m = max(m, abs_bits(a[r]));
+        }
+        m = max(m, static_cast<uint32_t>(__shfl_xor(m, 32, 64)));
+        const uint32_t byte = mx_scale_byte(m);
+        uint32_t h[4];  // four codes: half a word, whose other half the partner lane holds
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4)
+          h[q4] = mx_pair(a[4 * q4], a[4 * q4 + 1], byte) |
+                  (mx_pair(a[4 * q4 + 2], a[4 * q4 + 3], byte) << 8);
+        // half 0 stores words 0 and 1, half 1 words 2 and 3
+        const uint32_t give = g == 0 ? h[2] | (h[3] << 16) : h[0] | (h[1] << 16);
+        const uint32_t got = __shfl_xor(give, 32, 64);
+        uint2 w;
+        w.x = g == 0 ? h[0] | (got << 16) : (got & 0xFFFFu) | (h[2] << 16);
+        w.y = g == 0 ? h[1] | (got & 0xFFFF0000u) : (got >> 16) | (h[3] << 16);
+        if (blk * 32 < I) {
+          *reinterpret_cast<uint2*>(p.act_codes + static_cast<int64_t>(row) * (I / 2) + blk * 16 +
+                                    g * 8) = w;
+          if (g == 0)
+            store_scale(p.act_scales + static_cast<int64_t>(row) * sb, blk, I / 32, sb, byte);
+        }
+      }
+    }
+  }
+}
+
+using Tile32 = TileShape<256, 32, 4, 1, 2>;
+using Tile64 = TileShape<128, 64, 2, 2, 3>;
+using Tile128 = TileShape<128, 128, 2, 2, 2>;
+using Tile256 = TileShape<256, 256, 2, 4, 2>;
+
+template <typename S>
+void launch_tiles(const MxGemmArgs& a, hipStream_t stream) {
+  const bool gate_up = a.act_codes != nullptr;
+  const int cols = gate_up ? S::BW / 2 : S::BW, width = gate_up ? a.N / 2 : a.N;
+  const int n_tiles = (width + cols - 1) / cols;
+  const int64_t m_tiles = a.rows / S::BT + (a.E < a.rows ? a.E : a.rows);
+  const dim3 grid(static_cast<unsigned>((m_tiles * n_tiles + 7) / 8 * 8)), block(64 * S::kWaves);
+  if (gate_up) {
+    hipLaunchKernelGGL((mx_tile_kernel<S, true, F32>), grid, block, 0, stream, a, n_tiles);
+    return;
+  }
+  with_dtype(a.out_dtype, [&](auto t) {
+    using T = decltype(t);
+    hipLaunchKernelGGL((mx_tile_kernel<S, false, T>), grid, block, 0, stream, a, n_tiles);
+  });
+}
+
+void launch_stream(const MxGemmArgs& a, hipStream_t stream) {
   const bool gate_up = a.act_codes != nullptr;
   const int n_tiles = gate_up ? a.N / 64 : (a.N + 63) / 64;
   // an expert's last tile may be partial: at most one more tile per expert
@@ -165,6 +454,25 @@ void launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
     using T = decltype(t);
     hipLaunchKernelGGL((mx_stream_kernel<false, T>), grid, dim3(256), 0, stream, a, n_tiles);
   });
+}
+
+}  // namespace
+
+void launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
+  // mean rows per expert that can hold one
+  const int mean = a.rows / (a.E < a.rows ? a.E : a.rows);
+  // the tile kernels address mapped rows of A with 31-bit offsets
+  const bool far = a.row_slots != nullptr && a.a_rows * (a.K / 2) >= (static_cast<int64_t>(1) << 31);
+  if (mean <= 8 || far)
+    launch_stream(a, stream);
+  else if (mean <= 24)
+    launch_tiles<Tile32>(a, stream);
+  else if (mean <= 48)
+    launch_tiles<Tile64>(a, stream);
+  else if (mean < 512)
+    launch_tiles<Tile128>(a, stream);
+  else
+    launch_tiles<Tile256>(a, stream);
 }
 
 }  // namespace moe

@@ -46,23 +46,27 @@ __device__ __forceinline__ int64_t a_row(const MxGemmArgs& p, int r) {
   return t < p.a_rows ? t : -1;
 }
 
-// Tile `mt` of `size` rows in the sequence of all experts' tiles, experts
-// ascending: its expert and rows [r0, r1).  False behind the last tile.  The
-// whole wave searches: each lane counts the tiles of its share of experts, a
-// scan over the lanes finds the one that holds mt.  Offsets are held inside
+// The experts' rows cut into tiles of `size`, experts ascending; an expert's
+// last tile may be short.  The whole wave counts: each lane the tiles of its
+// share of experts, then a scan over the lanes.  Offsets are held inside
 // [0, rows], so damaged ones cannot lead out of the tensors.
-__device__ __forceinline__ bool find_tile(const int* __restrict__ offsets, int E, int rows,
-                                          int size, int mt, int& e, int& r0, int& r1) {
+struct Tiles {
+  const int* offsets;
+  int E, rows, size;
+  int inc, sum;  // this lane's share: tiles up to its end, tiles in it
+  int total;
+};
+
+__device__ __forceinline__ Tiles count_tiles(const int* __restrict__ offsets, int E, int rows,
+                                             int size) {
+  Tiles t{offsets, E, rows, size, 0, 0, 0};
   if (offsets == nullptr) {
-    e = 0;
-    r0 = mt * size;
-    r1 = min(rows, r0 + size);
-    return r0 < rows;
+    t.total = (rows + size - 1) / size;
+    return t;
   }
   const int lane = threadIdx.x & 63;
   const int per = (E + 63) >> 6;
   constexpr int kFly = 8;
-  int sum = 0;
   for (int i0 = 0; i0 < per; i0 += kFly) {
     int o[kFly + 1];
 #pragma unroll
@@ -71,25 +75,35 @@ __device__ __forceinline__ bool find_tile(const int* __restrict__ offsets, int E
       o[i] = min(max(offsets[at], 0), rows);
     }
 #pragma unroll
-    for (int i = 0; i < kFly; ++i) sum += (max(o[i + 1] - o[i], 0) + size - 1) / size;
+    for (int i = 0; i < kFly; ++i) t.sum += (max(o[i + 1] - o[i], 0) + size - 1) / size;
   }
-  int inc = sum;
+  t.inc = t.sum;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(inc, d, 64);
-    if (lane >= d) inc += v;
+    const int v = __shfl_up(t.inc, d, 64);
+    if (lane >= d) t.inc += v;
   }
-  const unsigned long long past = __ballot(inc > mt);
-  if (past == 0) return false;
-  const int owner = __builtin_ctzll(past);
-  int at = __builtin_amdgcn_readlane(inc - sum, owner);  // tiles before the owner's experts
-  e = owner * per;
-  for (;; ++e) {
-    const int a = min(max(offsets[e], 0), rows), b = min(max(offsets[e + 1], 0), rows);
-    const int n = (max(b - a, 0) + size - 1) / size;
-    if (mt < at + n || e + 1 >= E) {
-      r0 = a + (mt - at) * size;
-      r1 = min(b, r0 + size);
+  t.total = __builtin_amdgcn_readlane(t.inc, 63);
+  return t;
+}
+
+// Tile mt's expert and rows [r0, r1); false behind the last tile.
+__device__ __forceinline__ bool find_tile(const Tiles& t, int mt, int& e, int& r0, int& r1) {
+  if (mt >= t.total) return false;
+  if (t.offsets == nullptr) {
+    e = 0;
+    r0 = mt * t.size;
+    r1 = min(t.rows, r0 + t.size);
+    return true;
+  }
+  const int owner = __builtin_ctzll(__ballot(t.inc > mt));
+  int at = __builtin_amdgcn_readlane(t.inc - t.sum, owner);  // tiles before the owner's experts
+  for (e = owner * ((t.E + 63) >> 6);; ++e) {
+    const int a = min(max(t.offsets[e], 0), t.rows), b = min(max(t.offsets[e + 1], 0), t.rows);
+    const int n = (max(b - a, 0) + t.size - 1) / t.size;
+    if (mt < at + n || e + 1 >= t.E) {
+      r0 = a + (mt - at) * t.size;
+      r1 = min(b, r0 + t.size);
       return r0 < r1;
     }
     at += n;
