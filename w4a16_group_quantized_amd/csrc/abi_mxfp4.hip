@@ -82,7 +82,8 @@ int moe_mxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int32_t K, in
   if (int st = check_matrix(rows, K, x_stride, dtype)) return st;
   if (rows == 0) return MOE_OK;
   if (!ok_typed(x, dtype) || !ok_ptr(codes) || !ok_ptr(scales)) return MOE_ERR_INVALID_ARG;
-  launch_mx_quantize(x, dtype, rows, K, x_stride, codes, scales, static_cast<hipStream_t>(stream));
+  launch_mx_quantize(x, dtype, rows, K, x_stride, codes, scales, nullptr, 0, 0,
+                     static_cast<hipStream_t>(stream));
   return check_launch();
 }
 
@@ -289,8 +290,8 @@ static MxLayerWs mx_layer_ws(void* base, int64_t T, int32_t top_k, int32_t E, in
   w.num_active = reinterpret_cast<int32_t*>(take(4));
   w.perm_bytes = permute_workspace_bytes(T, E);
   w.perm = take(w.perm_bytes);
-  w.x_codes = reinterpret_cast<int32_t*>(take(static_cast<size_t>(T) * (H / 2)));
-  w.x_scales = reinterpret_cast<uint8_t*>(take(static_cast<size_t>(T) * mx_scale_bytes(H)));
+  w.x_codes = reinterpret_cast<int32_t*>(take(S * (H / 2)));
+  w.x_scales = reinterpret_cast<uint8_t*>(take(S * mx_scale_bytes(H)));
   w.act_codes = reinterpret_cast<int32_t*>(take(S * (I / 2)));
   w.act_scales = reinterpret_cast<uint8_t*>(take(S * mx_scale_bytes(I)));
   w.y = reinterpret_cast<float*>(take(4 * S * static_cast<size_t>(H)));
@@ -304,7 +305,7 @@ static int check_mx_layer(int64_t T, int32_t top_k, int32_t E, int32_t H, int32_
   if (E < 1 || top_k > E || H <= 0 || H % kGroup || I <= 0 || I % kGroup) return MOE_ERR_INVALID_ARG;
   if (E > kMaxExperts || H > kMaxColumns || I > kMaxColumns / 2) return MOE_ERR_UNSUPPORTED;
   const int64_t S = T * top_k;
-  if (int st = check_product(T, S, top_k, true, true, E, 2 * I, H)) return st;
+  if (int st = check_product(S, S, 1, false, true, E, 2 * I, H)) return st;
   return check_product(S, S, 1, false, true, E, H, I);
 }
 
@@ -329,9 +330,11 @@ int moe_mxfp4_layer_forward(const float* logits, const void* x, int32_t dtype, i
   if (int st = moe_route_permute(logits, T, E, top_k, w.ids, w.weights, w.offsets, w.sorted,
                                  w.slot_rows, w.active, w.num_active, w.perm, w.perm_bytes, stream))
     return st;
-  if (int st = moe_mxfp4_quantize(x, dtype, T, H, H, w.x_codes, w.x_scales, stream)) return st;
-  if (int st = moe_mxfp4_gate_up(w.x_codes, w.x_scales, T, w.sorted, top_k, S, w.offsets, E,
-                                 w13_codes, w13_scales, I, H, w.act_codes, w.act_scales, stream))
+  // every token once, stored to its rows: the products then read rows in order
+  launch_mx_quantize(x, dtype, T, H, H, w.x_codes, w.x_scales, w.slot_rows, top_k,
+                     static_cast<int>(S), static_cast<hipStream_t>(stream));
+  if (int st = moe_mxfp4_gate_up(w.x_codes, w.x_scales, S, nullptr, 1, S, w.offsets, E, w13_codes,
+                                 w13_scales, I, H, w.act_codes, w.act_scales, stream))
     return st;
   if (int st = moe_mxfp4_grouped_gemm(w.act_codes, w.act_scales, S, nullptr, 1, S, w.offsets, E,
                                       w2_codes, w2_scales, H, I, w.y, MOE_F32, H, stream))

@@ -11,8 +11,10 @@ namespace moe {
 // 32-bit words so that a lane takes the scales of 128 values with one load.
 __host__ __device__ constexpr int mx_scale_bytes(int K) { return 4 * ((K + 127) / 128); }
 
+// slot_rows (nullable): row t goes to rows slot_rows[t top_k + j] < out_rows.
 void launch_mx_quantize(const void* x, int dtype, int64_t rows, int K, int64_t ld, int32_t* codes,
-                        uint8_t* scales, hipStream_t stream);
+                        uint8_t* scales, const int* slot_rows, int top_k, int out_rows,
+                        hipStream_t stream);
 void launch_mx_dequantize(const int32_t* codes, const uint8_t* scales, int64_t rows, int K, void* x,
                           int dtype, int64_t ld, hipStream_t stream);
 

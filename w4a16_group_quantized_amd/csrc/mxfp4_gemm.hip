@@ -152,18 +152,19 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxGemmArgs p, int n_tile
 }
 
 // ------------------------------------------------------------------- tiles --
-// More rows per expert: a workgroup takes BW weight rows x BT tokens and walks
-// K in chunks of 256 values (128 bytes of codes and 8 of scales per row).
-// Chunks go from memory straight to LDS (no registers in between), STAGES of
-// them: chunk c + STAGES - 1 is requested while chunk c is multiplied, one
-// barrier per chunk.  In LDS a row's eight 16-byte blocks are stored with
-// their number xor (row mod 8), so the 16-byte reads of 8 neighbouring rows
-// meet different banks.  Each stage is an array of its own: the compiler then
-// knows that reading one does not wait for the loads into another.
+// A workgroup takes tiles of BW weight rows x BT tokens, one after the other,
+// and walks K in chunks of 256 values (128 bytes of codes and 8 of scales per
+// row).  Chunks go from memory straight to LDS (no registers in between) in a
+// ring of STAGES: the next one is requested as soon as its place is free, one
+// barrier per chunk, and the sequence of chunks runs on over the tiles, so the
+// loads of a tile are on their way while the one before is multiplied and
+// stored.  In LDS a row's eight 16-byte blocks are stored with their number
+// xor (row mod 8), so the 16-byte reads of 8 neighbouring rows meet different
+// banks.
 //
-// Rows behind a segment or behind N are loaded as they come (or not at all,
-// past the descriptors' ranges): each result depends on its own row and token
-// only, and theirs are not stored.
+// Tokens behind a segment and weight rows behind N leave what LDS holds, or
+// rows that follow: each result depends on its own row and token only, and
+// theirs are not stored.
 template <int BW_, int BT_, int WW_, int WT_, int STAGES_>
 struct TileShape {
   static constexpr int BW = BW_, BT = BT_, WW = WW_, WT = WT_, STAGES = STAGES_;
@@ -175,17 +176,46 @@ struct TileShape {
   static constexpr int kScaleW = (BW / 32 + kWaves - 1) / kWaves;
   static constexpr int kScaleT = (BT / 32 + kWaves - 1) / kWaves;
   static constexpr int kLoads = kLoadW + kLoadT + kScaleW + kScaleT;  // per wave and chunk
+  static constexpr int kPerCu = static_cast<int>(kGfx950LdsBytes) / (STAGES * kStage);
+  static_assert(STAGES * kStage <= static_cast<int>(kGfx950LdsBytes), "the ring fits in LDS");
   static_assert(kLoadW * kWaves * 8 == BW && kLoadT * kWaves * 8 == BT, "loads divide evenly");
 };
 
-typedef __attribute__((address_space(3))) void lds_void;
+// Loads from memory straight to LDS, 16 or 4 bytes per lane: from the lane's
+// offset `at` to consecutive places from LDS address `lds` on.  Written out
+// because the compiler, which does not see which stage a read of LDS meets,
+// would wait for every load on its way before it; the waits are
+// wait_loads_and_barrier's.  There is no result register that could be reused
+// too early, and the LDS arrays' addresses are taken, so what the memory
+// barriers of the waits cover includes them.
+struct Descriptor {
+  dwords4 d;
+};
 
-// 16 or 4 bytes per lane, from the lane's offset to consecutive places from dst on.
-__device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t at) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, static_cast<int>(at), 0, 0, 0);
+__device__ __forceinline__ Descriptor descriptor(const void* base, uint32_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  Descriptor r;
+  r.d[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at));
+  r.d[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32)) & 0xFFFFu;
+  r.d[2] = __builtin_amdgcn_readfirstlane(bytes);
+  r.d[3] = kRawBuffer;
+  return r;
 }
-__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* dst, uint32_t at) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, static_cast<int>(at), 0, 0, 0);
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) const void*)p));
+}
+
+__device__ __forceinline__ void load16_to_lds(const Descriptor& r, uint32_t lds, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
+               "v"(at), "s"(r.d)
+               : "m0");
+}
+__device__ __forceinline__ void load4_to_lds(const Descriptor& r, uint32_t lds, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds),
+               "v"(at), "s"(r.d)
+               : "m0");
 }
 
 template <int N>
@@ -198,120 +228,169 @@ __device__ __forceinline__ void wait_loads_and_barrier() {
   asm volatile("" ::: "memory");
 }
 
+__device__ __forceinline__ void wait_lds_and_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS only
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 template <typename S, bool GATE_UP, typename TO>
 __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, int n_tiles) {
-  __shared__ __attribute__((aligned(16))) uint8_t st0[S::kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t st1[S::kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t st2[S::STAGES > 2 ? S::kStage : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t ring[S::STAGES * S::kStage];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ww = wave / S::WT, wt = wave % S::WT;
 
-  // Tiles in groups of kGroup token tiles, tokens fastest, and each XCD (the
-  // workgroups of equal index mod 8) a contiguous run of them: the tiles that
-  // run together share weight rows and tokens in its L2.
+  // Tiles in groups of kGroupTiles token tiles, tokens fastest, and each XCD
+  // (the workgroups of equal index mod 8) a contiguous run of them: the tiles
+  // that run together share weight rows and tokens in its L2.
   constexpr int kGroupTiles = 4;
   const Tiles tiles = count_tiles(p.offsets, p.E, p.rows, S::BT);
   const int all = tiles.total * n_tiles;
   const int run = (all + 7) >> 3;
-  const int q = blockIdx.x >> 3;
-  const int tile = (blockIdx.x & 7) * run + q;
-  if (q >= run || tile >= all) return;
-  const int grp = tile / (kGroupTiles * n_tiles);
-  const int in = tile - grp * kGroupTiles * n_tiles;
-  const int gm = min(kGroupTiles, tiles.total - grp * kGroupTiles);
-  const int nt = in / gm;
-  int e, r0, r1;
-  if (!find_tile(tiles, grp * kGroupTiles + in - nt * gm, e, r0, r1)) return;
+  const int run0 = (blockIdx.x & 7) * run;
+  const int run_n = min(run, all - run0);
+  const int first_tile = blockIdx.x >> 3, step = gridDim.x >> 3;
+  if (first_tile >= run_n) return;
+  const int mine = (run_n - first_tile + step - 1) / step;
+  struct Tile {
+    int nt, e, r0, r1;
+  };
+  auto locate = [&](int j) {
+    const int tile = run0 + first_tile + j * step;
+    const int grp = tile / (kGroupTiles * n_tiles);
+    const int in = tile - grp * kGroupTiles * n_tiles;
+    const int gm = min(kGroupTiles, tiles.total - grp * kGroupTiles);
+    Tile t{in / gm, 0, 0, 0};
+    find_tile(tiles, grp * kGroupTiles + in - t.nt * gm, t.e, t.r0, t.r1);
+    return t;
+  };
 
-  const int blocks = p.K / 32;
+  const int blocks = p.K / 32, chunks = (blocks + 7) / 8;
   const int row_bytes = p.K / 2, sbytes = mx_scale_bytes(p.K);
   const int I = p.N / 2;
-  // Weight row of tile row rr: gate/up alternates 32 gate and 32 up rows.
-  auto w_row = [&](int rr) {
-    if constexpr (GATE_UP)
-      return ((rr >> 5) & 1) * I + nt * (S::BW / 2) + (rr >> 6) * 32 + (rr & 31);
-    else
-      return nt * S::BW + rr;
-  };
-  const auto rw = make_rsrc(p.w_codes + static_cast<int64_t>(e) * p.N * row_bytes,
-                            static_cast<uint32_t>(p.N) * row_bytes);
-  const auto rws = make_rsrc(p.w_scales + static_cast<int64_t>(e) * p.N * sbytes,
-                             static_cast<uint32_t>(p.N) * sbytes);
-  const int64_t first = p.row_slots == nullptr ? r0 : 0;
-  auto clip = [](int64_t n) {
-    return static_cast<uint32_t>(n < INT32_MAX ? n : INT32_MAX);
-  };
-  const auto ra = make_rsrc(p.a_codes + first * row_bytes, clip((p.a_rows - first) * row_bytes));
-  const auto ras = make_rsrc(p.a_scales + first * sbytes, clip((p.a_rows - first) * sbytes));
-  auto t_row = [&](int tr) -> uint32_t {  // row of A, relative to `first`
-    if (p.row_slots == nullptr) return tr;
-    const int64_t a = r0 + tr < r1 ? a_row(p, r0 + tr) : -1;
-    return a < 0 ? 0u : static_cast<uint32_t>(a);
-  };
 
+  // ---- loads: the tile and chunk that are requested next
+  Descriptor rw, rws, ra, ras;
   uint32_t at_w[S::kLoadW], at_t[S::kLoadT], at_ws[S::kScaleW], at_ts[S::kScaleT];
   // the 32 rows whose scales this wave loads; spare waves repeat a load
   auto scale_set = [&](int i, int sets) { return (i * S::kWaves + wave) % sets; };
+  auto aim = [&](const Tile& t) {
+    rw = descriptor(p.w_codes + static_cast<int64_t>(t.e) * p.N * row_bytes,
+                    static_cast<uint32_t>(p.N) * row_bytes);
+    rws = descriptor(p.w_scales + static_cast<int64_t>(t.e) * p.N * sbytes,
+                     static_cast<uint32_t>(p.N) * sbytes);
+    const int64_t first = p.row_slots == nullptr ? t.r0 : 0;
+    auto clip = [](int64_t n) { return static_cast<uint32_t>(n < INT32_MAX ? n : INT32_MAX); };
+    ra = descriptor(p.a_codes + first * row_bytes, clip((p.a_rows - first) * row_bytes));
+    ras = descriptor(p.a_scales + first * sbytes, clip((p.a_rows - first) * sbytes));
+    // Weight row of tile row rr: gate/up alternates 32 gate and 32 up rows.
+    auto w_row = [&](int rr) -> uint32_t {
+      if constexpr (GATE_UP)
+        return ((rr >> 5) & 1) * I + t.nt * (S::BW / 2) + (rr >> 6) * 32 + (rr & 31);
+      else
+        return t.nt * S::BW + rr;
+    };
+    // Offset of tile row tr's row of A in units of `bytes`; a row behind the
+    // segment, or without a token, is not read.
+    auto t_at = [&](int tr, int bytes) -> uint32_t {
+      if (t.r0 + tr >= t.r1) return kOutOfRange;
+      if (p.row_slots == nullptr) return static_cast<uint32_t>(tr) * bytes;
+      const int64_t a = a_row(p, t.r0 + tr);
+      return a < 0 ? kOutOfRange : static_cast<uint32_t>(a) * bytes;
+    };
 #pragma unroll
-  for (int i = 0; i < S::kLoadW; ++i) {
-    const int rr = (i * S::kWaves + wave) * 8 + (lane >> 3);
-    at_w[i] = static_cast<uint32_t>(w_row(rr)) * row_bytes + ((lane ^ rr) & 7) * 16;
-  }
+    for (int i = 0; i < S::kLoadW; ++i) {
+      const int rr = (i * S::kWaves + wave) * 8 + (lane >> 3);
+      at_w[i] = w_row(rr) * row_bytes + ((lane ^ rr) & 7) * 16;
+    }
 #pragma unroll
-  for (int i = 0; i < S::kLoadT; ++i) {
-    const int tr = (i * S::kWaves + wave) * 8 + (lane >> 3);
-    at_t[i] = t_row(tr) * row_bytes + ((lane ^ tr) & 7) * 16;
-  }
-#pragma unroll
-  for (int i = 0; i < S::kScaleW; ++i)
-    at_ws[i] = static_cast<uint32_t>(w_row(scale_set(i, S::BW / 32) * 32 + (lane >> 1))) * sbytes +
-               (lane & 1) * 4;
-#pragma unroll
-  for (int i = 0; i < S::kScaleT; ++i)
-    at_ts[i] = t_row(scale_set(i, S::BT / 32) * 32 + (lane >> 1)) * sbytes + (lane & 1) * 4;
-
-  auto load = [&](uint8_t* st, int c) {
-#pragma unroll
-    for (int i = 0; i < S::kLoadW; ++i)
-      load16_to_lds(rw, st + (i * S::kWaves + wave) * 1024, at_w[i] + c * 128);
-#pragma unroll
-    for (int i = 0; i < S::kLoadT; ++i)
-      load16_to_lds(ra, st + S::BW * 128 + (i * S::kWaves + wave) * 1024, at_t[i] + c * 128);
+    for (int i = 0; i < S::kLoadT; ++i) {
+      const int tr = (i * S::kWaves + wave) * 8 + (lane >> 3);
+      at_t[i] = t_at(tr, row_bytes) + ((lane ^ tr) & 7) * 16;
+    }
 #pragma unroll
     for (int i = 0; i < S::kScaleW; ++i)
-      load4_to_lds(rws, st + S::kCodes + scale_set(i, S::BW / 32) * 256, at_ws[i] + c * 8);
+      at_ws[i] = w_row(scale_set(i, S::BW / 32) * 32 + (lane >> 1)) * sbytes + (lane & 1) * 4;
 #pragma unroll
     for (int i = 0; i < S::kScaleT; ++i)
-      load4_to_lds(ras, st + S::kCodes + S::BW * 8 + scale_set(i, S::BT / 32) * 256, at_ts[i] + c * 8);
+      at_ts[i] = t_at(scale_set(i, S::BT / 32) * 32 + (lane >> 1), sbytes) + (lane & 1) * 4;
+  };
+  int load_tile = 0, load_chunk = 0;
+  uint32_t load_at = lds_address(ring);
+  const uint32_t ring_at = load_at;
+  // Requests the next chunk.  Behind the last one the loads go to empty ranges
+  // (nothing is fetched), so that the number on their way is always the same.
+  auto load_next = [&]() {
+#pragma unroll
+    for (int i = 0; i < S::kLoadW; ++i) {
+      load16_to_lds(rw, load_at + (i * S::kWaves + wave) * 1024, at_w[i]);
+      at_w[i] += 128;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kLoadT; ++i) {
+      load16_to_lds(ra, load_at + S::BW * 128 + (i * S::kWaves + wave) * 1024, at_t[i]);
+      at_t[i] += 128;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kScaleW; ++i) {
+      load4_to_lds(rws, load_at + S::kCodes + scale_set(i, S::BW / 32) * 256, at_ws[i]);
+      at_ws[i] += 8;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kScaleT; ++i) {
+      load4_to_lds(ras, load_at + S::kCodes + S::BW * 8 + scale_set(i, S::BT / 32) * 256, at_ts[i]);
+      at_ts[i] += 8;
+    }
+    load_at += S::kStage;
+    if (load_at == ring_at + S::STAGES * S::kStage) load_at = ring_at;
+    if (++load_chunk == chunks) {
+      load_chunk = 0;
+      if (++load_tile < mine)
+        aim(locate(load_tile));
+      else
+        rw.d[2] = rws.d[2] = ra.d[2] = ras.d[2] = 0;
+    }
   };
 
+  // ---- products
   const int col = lane & 31, g = lane >> 5;
-  f32x16 acc[S::NW][S::NT] = {};
+  f32x16 acc[S::NW][S::NT];
   // Step s multiplies blocks 2s and 2s + 1 of the chunk, lane half g taking
-  // block 2s + g; its scale byte is byte 2s + g of the row's eight.
+  // block 2s + g; its scale byte is byte 2s + g of the row's eight.  The places
+  // of the fragments of one side differ by whole 32 rows (4096 bytes).
+  uint32_t at_w4[4], at_t4[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const uint32_t in_rows = col * 128 + (((2 * s + g) ^ col) & 7) * 16;
+    at_w4[s] = ww * S::NW * 4096 + in_rows;
+    at_t4[s] = S::BW * 128 + wt * S::NT * 4096 + in_rows;
+  }
+  const uint32_t at_w1 = S::kCodes + (ww * S::NW * 32 + col) * 8;
+  const uint32_t at_t1 = S::kCodes + (S::BW + wt * S::NT * 32 + col) * 8;
   auto compute = [&](const uint8_t* st) {
-    auto frag = [&](int row, int s) {
-      return *reinterpret_cast<const dwords4*>(st + row * 128 + (((2 * s + g) ^ row) & 7) * 16);
+    auto frag = [&](uint32_t at, int i) {
+      return *reinterpret_cast<const dwords4*>(st + at + i * 4096);
     };
-    auto scale = [&](int row) {
-      uint2 v = *reinterpret_cast<const uint2*>(st + S::kCodes + row * 8);
+    auto scale = [&](uint32_t at, int i) {
+      uint2 v = *reinterpret_cast<const uint2*>(st + at + i * 256);
       v.x >>= 8 * g;
       v.y >>= 8 * g;
       return v;
     };
     uint2 ws[S::NW], ts[S::NT];
 #pragma unroll
-    for (int i = 0; i < S::NW; ++i) ws[i] = scale((ww * S::NW + i) * 32 + col);
+    for (int i = 0; i < S::NW; ++i) ws[i] = scale(at_w1, i);
 #pragma unroll
-    for (int i = 0; i < S::NT; ++i) ts[i] = scale(S::BW + (wt * S::NT + i) * 32 + col);
-    auto step = [&](auto sc) {
+    for (int i = 0; i < S::NT; ++i) ts[i] = scale(at_t1, i);
+    auto multiply = [&](auto sc) {
       constexpr int s = decltype(sc)::value;
       dwords4 w[S::NW], t[S::NT];
 #pragma unroll
-      for (int i = 0; i < S::NW; ++i) w[i] = frag((ww * S::NW + i) * 32 + col, s);
+      for (int i = 0; i < S::NW; ++i) w[i] = frag(at_w4[s], i);
 #pragma unroll
-      for (int i = 0; i < S::NT; ++i) t[i] = frag(S::BW + (wt * S::NT + i) * 32 + col, s);
+      for (int i = 0; i < S::NT; ++i) t[i] = frag(at_t4[s], i);
 #pragma unroll
       for (int i = 0; i < S::NW; ++i)
 #pragma unroll
@@ -320,10 +399,10 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
               operand(w[i]), operand(t[j]), acc[i][j], kFp4, kFp4, 2 * (s & 1),
               s < 2 ? ws[i].x : ws[i].y, 2 * (s & 1), s < 2 ? ts[j].x : ts[j].y);
     };
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 1>{});
-    step(std::integral_constant<int, 2>{});
-    step(std::integral_constant<int, 3>{});
+    multiply(std::integral_constant<int, 0>{});
+    multiply(std::integral_constant<int, 1>{});
+    multiply(std::integral_constant<int, 2>{});
+    multiply(std::integral_constant<int, 3>{});
   };
   // A last chunk of fewer than 8 blocks: the others become zeros of scale 1.
   auto cut = [&](uint8_t* st, int live) {
@@ -335,102 +414,114 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
     }
   };
 
-  const int chunks = (blocks + 7) / 8;
-  auto stage = [&](uint8_t* cur, uint8_t* next, int c) {
-    // the newest STAGES - 2 chunks may still be on their way, near the end fewer
-    if (c + S::STAGES - 2 < chunks)
-      wait_loads_and_barrier<(S::STAGES - 2) * S::kLoads>();
-    else
-      wait_loads_and_barrier<0>();
-    if (blocks - 8 * c < 8) {
-      cut(cur, blocks - 8 * c);
-      wait_loads_and_barrier<0>();
-    }
-    if (c + S::STAGES - 1 < chunks) load(next, c + S::STAGES - 1);
-    compute(cur);
-  };
-  load(st0, 0);
-  if constexpr (S::STAGES == 2) {
-    for (int c = 0; c < chunks; c += 2) {
-      stage(st0, st1, c);
-      if (c + 1 < chunks) stage(st1, st0, c + 1);
-    }
-  } else {
-    if (chunks > 1) load(st1, 1);
-    for (int c = 0; c < chunks; c += 3) {
-      stage(st0, st2, c);
-      if (c + 1 < chunks) stage(st1, st0, c + 1);
-      if (c + 2 < chunks) stage(st2, st1, c + 2);
-    }
-  }
-
   // acc[i][j][4 q + r] is weight row 32 i' + 8 q + 4 g + r of token 32 j' + col
+  auto store = [&](const Tile& tl) {
 #pragma unroll
-  for (int j = 0; j < S::NT; ++j) {
-    const int row = r0 + (wt * S::NT + j) * 32 + col;
-    if (row >= r1) continue;  // both lane halves of a token alike
-    const bool none = p.row_slots != nullptr && a_row(p, row) < 0;
-    if constexpr (!GATE_UP) {
-      auto* o = static_cast<typename TO::bits*>(p.out) + row * p.out_ld;
+    for (int j = 0; j < S::NT; ++j) {
+      const int row = tl.r0 + (wt * S::NT + j) * 32 + col;
+      if (row >= tl.r1) continue;  // both lane halves of a token alike
+      const bool none = p.row_slots != nullptr && a_row(p, row) < 0;
+      if constexpr (!GATE_UP) {
+        auto* o = static_cast<typename TO::bits*>(p.out) + row * p.out_ld;
 #pragma unroll
-      for (int i = 0; i < S::NW; ++i)
+        for (int i = 0; i < S::NW; ++i)
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          const int n0 = nt * S::BW + (ww * S::NW + i) * 32 + 8 * q4 + 4 * g;
-          f32x4 v;
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const int n0 = tl.nt * S::BW + (ww * S::NW + i) * 32 + 8 * q4 + 4 * g;
+            f32x4 v;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = none ? 0.f : acc[i][j][4 * q4 + r];
-          store4<TO>(o + n0, p.N - n0, v);
-        }
-    } else {
-      const int sb = mx_scale_bytes(I);
+            for (int r = 0; r < 4; ++r) v[r] = none ? 0.f : acc[i][j][4 * q4 + r];
+            store4<TO>(o + n0, p.N - n0, v);
+          }
+      } else {
+        const int sb = mx_scale_bytes(I);
 #pragma unroll
-      for (int i = 0; i < S::NW; i += 2) {
-        const int blk = nt * (S::BW / 64) + (ww * S::NW + i) / 2;
-        float a[16];
-        uint32_t m = 0;
+        for (int i = 0; i < S::NW; i += 2) {
+          const int blk = tl.nt * (S::BW / 64) + (ww * S::NW + i) / 2;
+          float a[16];
+          uint32_t m = 0;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          a[r] = none ? 0.f : silu_mul(acc[i][j][r], acc[i + 1][j][r]);
-          m = max(m, abs_bits(a[r]));
-        }
-        m = max(m, static_cast<uint32_t>(__shfl_xor(m, 32, 64)));
-        const uint32_t byte = mx_scale_byte(m);
-        uint32_t h[4];  // four codes: half a word, whose other half the partner lane holds
+          for (int r = 0; r < 16; ++r) {
+            a[r] = none ? 0.f : silu_mul(acc[i][j][r], acc[i + 1][j][r]);
+            m = max(m, abs_bits(a[r]));
+          }
+          m = max(m, static_cast<uint32_t>(__shfl_xor(m, 32, 64)));
+          const uint32_t byte = mx_scale_byte(m);
+          uint32_t h[4];  // four codes: half a word, whose other half the partner lane holds
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4)
-          h[q4] = mx_pair(a[4 * q4], a[4 * q4 + 1], byte) |
-                  (mx_pair(a[4 * q4 + 2], a[4 * q4 + 3], byte) << 8);
-        // half 0 stores words 0 and 1, half 1 words 2 and 3
-        const uint32_t give = g == 0 ? h[2] | (h[3] << 16) : h[0] | (h[1] << 16);
-        const uint32_t got = __shfl_xor(give, 32, 64);
-        uint2 w;
-        w.x = g == 0 ? h[0] | (got << 16) : (got & 0xFFFFu) | (h[2] << 16);
-        w.y = g == 0 ? h[1] | (got & 0xFFFF0000u) : (got >> 16) | (h[3] << 16);
-        if (blk * 32 < I) {
-          *reinterpret_cast<uint2*>(p.act_codes + static_cast<int64_t>(row) * (I / 2) + blk * 16 +
-                                    g * 8) = w;
-          if (g == 0)
-            store_scale(p.act_scales + static_cast<int64_t>(row) * sb, blk, I / 32, sb, byte);
+          for (int q4 = 0; q4 < 4; ++q4)
+            h[q4] = mx_pair(a[4 * q4], a[4 * q4 + 1], byte) |
+                    (mx_pair(a[4 * q4 + 2], a[4 * q4 + 3], byte) << 8);
+          // half 0 stores words 0 and 1, half 1 words 2 and 3
+          const uint32_t give = g == 0 ? h[2] | (h[3] << 16) : h[0] | (h[1] << 16);
+          const uint32_t got = __shfl_xor(give, 32, 64);
+          uint2 w;
+          w.x = g == 0 ? h[0] | (got << 16) : (got & 0xFFFFu) | (h[2] << 16);
+          w.y = g == 0 ? h[1] | (got & 0xFFFF0000u) : (got >> 16) | (h[3] << 16);
+          if (blk * 32 < I) {
+            *reinterpret_cast<uint2*>(p.act_codes + static_cast<int64_t>(row) * (I / 2) +
+                                      blk * 16 + g * 8) = w;
+            if (g == 0)
+              store_scale(p.act_scales + static_cast<int64_t>(row) * sb, blk, I / 32, sb, byte);
+          }
         }
       }
     }
+  };
+
+  aim(locate(0));
+#pragma unroll
+  for (int s = 0; s + 1 < S::STAGES; ++s) load_next();
+  Tile now{};
+  uint32_t stage = 0;
+  for (int j = 0, c = 0;;) {
+    // chunk c is there when only the STAGES - 2 chunks behind it are on their
+    // way (stores among them make the wait longer, never too short)
+    wait_loads_and_barrier<(S::STAGES - 2) * S::kLoads>();
+    load_next();
+    if (c == 0) {
+      if (j > 0) store(now);
+      if (j == mine) break;
+      now = locate(j);
+#pragma unroll
+      for (int i = 0; i < S::NW; ++i)
+#pragma unroll
+        for (int t = 0; t < S::NT; ++t) acc[i][t] = f32x16{};
+    }
+    uint8_t* st = ring + stage;
+    if (8 * (c + 1) > blocks) {
+      cut(st, blocks - 8 * c);
+      wait_lds_and_barrier();
+    }
+    compute(st);
+    stage = stage + S::kStage == S::STAGES * S::kStage ? 0 : stage + S::kStage;
+    if (++c == chunks) {
+      c = 0;
+      ++j;
+    }
   }
+  // no load into this workgroup's LDS outlives it
+  __builtin_amdgcn_s_waitcnt(0x0F70);
 }
 
-using Tile32 = TileShape<256, 32, 4, 1, 2>;
-using Tile64 = TileShape<128, 64, 2, 2, 3>;
-using Tile128 = TileShape<128, 128, 2, 2, 2>;
-using Tile256 = TileShape<256, 256, 2, 4, 2>;
+// Shapes, named by their tokens; 32 tokens in a deep ring and in a short one.
+using Tile32 = TileShape<128, 32, 2, 1, 3>;
+using Tile32Short = TileShape<128, 32, 2, 1, 2>;
+using Tile64 = TileShape<256, 64, 4, 2, 3>;
+using Tile128 = TileShape<256, 128, 4, 2, 3>;
+using Tile256 = TileShape<256, 256, 4, 2, 2>;
 
 template <typename S>
 void launch_tiles(const MxGemmArgs& a, hipStream_t stream) {
   const bool gate_up = a.act_codes != nullptr;
   const int cols = gate_up ? S::BW / 2 : S::BW, width = gate_up ? a.N / 2 : a.N;
   const int n_tiles = (width + cols - 1) / cols;
+  // at most one short tile per expert; no more workgroups than run at once
   const int64_t m_tiles = a.rows / S::BT + (a.E < a.rows ? a.E : a.rows);
-  const dim3 grid(static_cast<unsigned>((m_tiles * n_tiles + 7) / 8 * 8)), block(64 * S::kWaves);
-  if (gate_up) {
+  const int64_t resident = static_cast<int64_t>(device_info().cus) * S::kPerCu;
+  const int64_t groups = m_tiles * n_tiles < resident ? m_tiles * n_tiles : resident;
+  const dim3 grid(static_cast<unsigned>((groups + 7) / 8 * 8)), block(64 * S::kWaves);
+  if constexpr (S::NW % 2 == 0) if (gate_up) {
     hipLaunchKernelGGL((mx_tile_kernel<S, true, F32>), grid, block, 0, stream, a, n_tiles);
     return;
   }
@@ -459,20 +550,23 @@ void launch_stream(const MxGemmArgs& a, hipStream_t stream) {
 }  // namespace
 
 void launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
-  // mean rows per expert that can hold one
-  const int mean = a.rows / (a.E < a.rows ? a.E : a.rows);
+  const int active = a.E < a.rows ? a.E : a.rows;  // experts that can hold a row
+  const int mean = a.rows / active;
   // the tile kernels address mapped rows of A with 31-bit offsets
   const bool far = a.row_slots != nullptr && a.a_rows * (a.K / 2) >= (static_cast<int64_t>(1) << 31);
-  if (mean <= 8 || far)
-    launch_stream(a, stream);
-  else if (mean <= 24)
-    launch_tiles<Tile32>(a, stream);
-  else if (mean <= 48)
-    launch_tiles<Tile64>(a, stream);
-  else if (mean < 512)
-    launch_tiles<Tile128>(a, stream);
-  else
-    launch_tiles<Tile256>(a, stream);
+  const int64_t weights = static_cast<int64_t>(active) * a.N * (a.K / 2);
+  if (far || (mean <= 8 && weights <= 32 << 20)) return launch_stream(a, stream);
+  // the tile that holds the mean, or a smaller one where its tiles would leave
+  // compute units without any
+  const auto enough = [&](int bw, int bt) {
+    return static_cast<int64_t>(active) * ((mean + bt - 1) / bt) * ((a.N + bw - 1) / bw) >=
+           device_info().cus;
+  };
+  if (mean >= 512 && enough(256, 256)) return launch_tiles<Tile256>(a, stream);
+  if (mean > 48 && enough(256, 128)) return launch_tiles<Tile128>(a, stream);
+  if (mean > 24 && enough(256, 64)) return launch_tiles<Tile64>(a, stream);
+  if (a.K > 1024) return launch_tiles<Tile32>(a, stream);
+  launch_tiles<Tile32Short>(a, stream);
 }
 
 }  // namespace moe

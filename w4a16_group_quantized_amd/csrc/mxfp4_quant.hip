@@ -27,10 +27,13 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   return v > o ? v : o;
 }
 
-template <typename T>
+// SCATTER: row t goes to rows slot_rows[t top_k + j] < out_rows, j < top_k,
+// instead of row t (the rows of a token in expert order).
+template <typename T, bool SCATTER>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(
     const typename T::bits* __restrict__ x, int64_t rows, int words, int64_t ld,
-    uint32_t* __restrict__ codes, uint8_t* __restrict__ scales, int sbytes) {
+    uint32_t* __restrict__ codes, uint8_t* __restrict__ scales, int sbytes,
+    const int* __restrict__ slot_rows, int top_k, int out_rows) {
   const int64_t total = rows * words;
   constexpr int kPerBlock = kThreads * kUnroll;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * kPerBlock; base < total;
@@ -74,9 +77,18 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(
         q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[u][6] * inv, v[u][7] * inv, 1.f, 3);
       }
       if (row < rows) {
-        codes[row * words + c] = q;
-        if ((c & 3) == 0)
-          store_scale(scales + row * sbytes, c >> 2, words >> 2, sbytes, byte);
+        auto put = [&](int64_t to) {
+          codes[to * words + c] = q;
+          if ((c & 3) == 0) store_scale(scales + to * sbytes, c >> 2, words >> 2, sbytes, byte);
+        };
+        if constexpr (SCATTER) {
+          for (int j = 0; j < top_k; ++j) {
+            const int to = slot_rows[row * top_k + j];
+            if (static_cast<uint32_t>(to) < static_cast<uint32_t>(out_rows)) put(to);
+          }
+        } else {
+          put(row);
+        }
       }
     }
   }
@@ -130,15 +142,20 @@ int grid_for(int64_t rows, int words) {
 }  // namespace
 
 void launch_mx_quantize(const void* x, int dtype, int64_t rows, int K, int64_t ld, int32_t* codes,
-                        uint8_t* scales, hipStream_t stream) {
+                        uint8_t* scales, const int* slot_rows, int top_k, int out_rows,
+                        hipStream_t stream) {
   const int words = K / 8;
   const dim3 grid(grid_for(rows, words));
   with_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const auto* p = static_cast<const typename T::bits*>(x);
     auto* q = reinterpret_cast<uint32_t*>(codes);
-    hipLaunchKernelGGL(quantize_kernel<T>, grid, dim3(kThreads), 0, stream, p, rows, words,
-                       ld, q, scales, mx_scale_bytes(K));
+    if (slot_rows != nullptr)
+      hipLaunchKernelGGL((quantize_kernel<T, true>), grid, dim3(kThreads), 0, stream, p, rows, words,
+                         ld, q, scales, mx_scale_bytes(K), slot_rows, top_k, out_rows);
+    else
+      hipLaunchKernelGGL((quantize_kernel<T, false>), grid, dim3(kThreads), 0, stream, p, rows,
+                         words, ld, q, scales, mx_scale_bytes(K), slot_rows, top_k, out_rows);
   });
 }
 

@@ -47,42 +47,56 @@ __device__ __forceinline__ int64_t a_row(const MxGemmArgs& p, int r) {
 }
 
 // The experts' rows cut into tiles of `size`, experts ascending; an expert's
-// last tile may be short.  The whole wave counts: each lane the tiles of its
-// share of experts, then a scan over the lanes.  Offsets are held inside
+// last tile may be short.  The whole wave counts: lane l the tiles of experts
+// [l per, (l + 1) per), then a scan over the lanes.  Offsets are held inside
 // [0, rows], so damaged ones cannot lead out of the tensors.
+constexpr int kHeld = 8;  // experts per lane whose offsets stay in registers
+
 struct Tiles {
   const int* offsets;
   int E, rows, size;
-  int inc, sum;  // this lane's share: tiles up to its end, tiles in it
+  int per;             // experts per lane
+  int inc, sum;        // this lane's share: tiles up to its end, tiles in it
+  int o[kHeld + 1];    // its first offsets (all of them when per <= kHeld)
   int total;
 };
 
+__device__ __forceinline__ int tile_count(int a, int b, int size) {
+  return (max(b - a, 0) + size - 1) / size;
+}
+
+// Inclusive sum over the lanes up to this one.
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
 __device__ __forceinline__ Tiles count_tiles(const int* __restrict__ offsets, int E, int rows,
                                              int size) {
-  Tiles t{offsets, E, rows, size, 0, 0, 0};
+  Tiles t{offsets, E, rows, size, (E + 63) >> 6, 0, 0, {}, 0};
   if (offsets == nullptr) {
     t.total = (rows + size - 1) / size;
     return t;
   }
   const int lane = threadIdx.x & 63;
-  const int per = (E + 63) >> 6;
-  constexpr int kFly = 8;
-  for (int i0 = 0; i0 < per; i0 += kFly) {
-    int o[kFly + 1];
+  auto share = [&](int i0, int (&o)[kHeld + 1]) {
 #pragma unroll
-    for (int i = 0; i <= kFly; ++i) {
-      const int at = min(lane * per + min(i0 + i, per), E);
-      o[i] = min(max(offsets[at], 0), rows);
-    }
+    for (int i = 0; i <= kHeld; ++i)
+      o[i] = min(max(offsets[min(lane * t.per + min(i0 + i, t.per), E)], 0), rows);
 #pragma unroll
-    for (int i = 0; i < kFly; ++i) t.sum += (max(o[i + 1] - o[i], 0) + size - 1) / size;
+    for (int i = 0; i < kHeld; ++i) t.sum += tile_count(o[i], o[i + 1], size);
+  };
+  share(0, t.o);
+  for (int i0 = kHeld; i0 < t.per; i0 += kHeld) {
+    int o[kHeld + 1];
+    share(i0, o);
   }
-  t.inc = t.sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(t.inc, d, 64);
-    if (lane >= d) t.inc += v;
-  }
+  t.inc = wave_scan(t.sum);
   t.total = __builtin_amdgcn_readlane(t.inc, 63);
   return t;
 }
@@ -98,16 +112,37 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int mt, int& e, int& r
   }
   const int owner = __builtin_ctzll(__ballot(t.inc > mt));
   int at = __builtin_amdgcn_readlane(t.inc - t.sum, owner);  // tiles before the owner's experts
-  for (e = owner * ((t.E + 63) >> 6);; ++e) {
-    const int a = min(max(t.offsets[e], 0), t.rows), b = min(max(t.offsets[e + 1], 0), t.rows);
-    const int n = (max(b - a, 0) + t.size - 1) / t.size;
-    if (mt < at + n || e + 1 >= t.E) {
-      r0 = a + (mt - at) * t.size;
-      r1 = min(b, r0 + t.size);
-      return r0 < r1;
+  if (t.per <= kHeld) {
+    int b = __builtin_amdgcn_readlane(t.o[0], owner);
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int a = b;
+      b = __builtin_amdgcn_readlane(t.o[i + 1], owner);
+      const int n = tile_count(a, b, t.size);
+      if (!found && mt < at + n) {
+        found = true;
+        e = owner * t.per + i;
+        r0 = a + (mt - at) * t.size;
+        r1 = min(b, r0 + t.size);
+      }
+      at += n;
     }
-    at += n;
+    return found;
   }
+  // more experts per lane: the lanes share out the owner's
+  const int lane = threadIdx.x & 63;
+  const int mine = min(owner * t.per + min(lane, t.per), t.E);
+  const int a = min(max(t.offsets[mine], 0), t.rows);
+  const int b = min(max(t.offsets[min(mine + 1, t.E)], 0), t.rows);
+  const int n = lane < t.per ? tile_count(a, b, t.size) : 0;
+  const int inc = wave_scan(n);
+  const int who = __builtin_ctzll(__ballot(at + inc > mt));
+  at += __builtin_amdgcn_readlane(inc - n, who);
+  e = owner * t.per + who;
+  r0 = __builtin_amdgcn_readlane(a, who) + (mt - at) * t.size;
+  r1 = min(__builtin_amdgcn_readlane(b, who), r0 + t.size);
+  return true;
 }
 
 template <typename T>
@@ -133,8 +168,17 @@ __device__ __forceinline__ void store4(typename T::bits* p, int n, f32x4 v) {
 }
 
 // ---- the quantising epilogue ---------------------------------------------------
+// gate / (1 + e^-gate) * up in a dozen instructions (the library's exponential
+// and division made the epilogue the longest part of the gate/up product).
+// e^-gate = 2^t (1 + r ln 2), t = -gate log2(e) rounded and r what that rounding
+// left, so the exponential is good to 2 units in the last place at any gate;
+// the hardware's reciprocal to 1.
 __device__ __forceinline__ float silu_mul(float gate, float up) {
-  return gate / (1.f + expf(-gate)) * up;
+  constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147181f;
+  const float t = -gate * kLog2e;
+  const float r = fmaf(-gate, kLog2eRest, fmaf(-gate, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t) * fmaf(r, kLn2, 1.f);
+  return gate * __builtin_amdgcn_rcpf(1.f + e) * up;
 }
 __device__ __forceinline__ uint32_t abs_bits(float v) {
   return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu;

@@ -620,55 +620,89 @@ def weights_to_device(host: dict, device="cuda") -> dict:
 # --------------------------------------------------------------------------- #
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
+# The checks below run on every call of a few microseconds, so each asks a
+# tensor as little as it can; what went wrong is worked out only for a refusal.
 
-def _device_of(**tensors) -> torch.device:
-    """The one GPU that all the given tensors (None: absent) are on."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError(f"{name} is on {t.device}, not on a GPU")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the tensors before it on {dev}")
-        dev = t.device
+
+def _device_of(*tensors) -> int:
+    """Index of the one GPU that all the given tensors (None: absent) are on."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, not on a GPU")
+            if d != dev:
+                if dev >= 0:
+                    raise ValueError(f"a tensor of shape {tuple(t.shape)} is on GPU {d}, the ones "
+                                     f"before it on GPU {dev}")
+                dev = d
     return dev
 
 
-def _run(fn: str, dev: torch.device, *args) -> None:
-    lib = load_library()
-    if dev.index == torch.cuda.current_device():
-        status = getattr(lib, fn)(*args, torch.cuda.current_stream(dev).cuda_stream or None)
+_fns: dict = {}
+
+
+def _run(fn: str, dev: int, *args) -> None:
+    f = _fns.get(fn)
+    if f is None:
+        f = _fns[fn] = getattr(load_library(), fn)
+    # the device's current stream as torch keeps it, without an object around it
+    if dev == torch._C._cuda_getDevice():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib, fn)(*args, torch.cuda.current_stream(dev).cuda_stream or None)
-    _check(fn, status)
+            status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status != MOE_OK:
+        _check(fn, status)
 
 
-def _dense(name: str, t: torch.Tensor, dtype: torch.dtype, *shape) -> int | None:
-    """Pointer of a contiguous tensor of this type and shape (None in `shape`: any length)."""
-    if t.dtype != dtype:
+def _dense(name: str, t: torch.Tensor, dtype: torch.dtype, *shape) -> int:
+    """Pointer of a contiguous tensor of this type and shape."""
+    if t.dtype is not dtype:
         raise ValueError(f"{name} is {t.dtype}, not {dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() or None
+    return t.data_ptr()
 
 
-def _matrix(name: str, t: torch.Tensor, rows: int | None, cols: int | None):
-    """(pointer, dtype code, row stride) of a matrix with contiguous rows."""
-    if t.dtype not in _DTYPE:
+def _bytes(name: str, t: torch.Tensor | None):
+    """(pointer, bytes) of a workspace (None: none)."""
+    if t is None:
+        return None, 0
+    n = t.numel()
+    return _dense(name, t, torch.uint8, n), n
+
+
+def _matrix(name: str, t: torch.Tensor):
+    """(pointer, dtype code, row stride, rows, columns) of a matrix with contiguous rows."""
+    code = _DTYPE.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} is {t.dtype}, not float32, float16 or bfloat16")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (
-            cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(rows, cols)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} has shape {tuple(shape)}, not two dimensions")
+    rows, cols = shape
+    if t.is_contiguous():
+        return t.data_ptr(), code, cols, rows, cols
+    if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    stride = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-    if stride < t.shape[1]:
+    stride = t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    if stride < cols:
         raise ValueError(f"{name} has rows that overlap (stride {stride})")
-    return t.data_ptr() or None, _DTYPE[t.dtype], stride
+    return t.data_ptr(), code, stride, rows, cols
+
+
+def _sized(name: str, t: torch.Tensor, rows: int, cols: int, code: int | None = None):
+    """(pointer, dtype code, row stride) of such a matrix of a given shape (and type)."""
+    ptr, got, stride, r, c = _matrix(name, t)
+    if r != rows or c != cols:
+        raise ValueError(f"{name} has shape {(r, c)}, not {(rows, cols)}")
+    if code is not None and got != code:
+        raise ValueError(f"{name} is {t.dtype}, not the type of the tensor that it goes with")
+    return ptr, got, stride
 
 
 def _apart(name: str, out: torch.Tensor, **inputs) -> None:
@@ -679,12 +713,15 @@ def _apart(name: str, out: torch.Tensor, **inputs) -> None:
         stride = (t.stride(0) if rows > 1 else cols) * size
         return t.data_ptr(), stride, cols * size, (rows - 1) * stride + cols * size
 
-    if out.numel() == 0:
-        return
-    a, a_stride, a_cols, a_span = place(out)
+    a, dense = out.data_ptr(), out.is_contiguous()
     for other, t in inputs.items():
-        if t.numel() == 0:
+        if dense and t.is_contiguous():  # the usual case, at the least cost
+            b = t.data_ptr()
+            if a + out.nbytes <= b or b + t.nbytes <= a:
+                continue
+        if out.numel() == 0 or t.numel() == 0:
             continue
+        a, a_stride, a_cols, a_span = place(out)
         b, b_stride, b_cols, b_span = place(t)
         if a + a_span <= b or b + b_span <= a:
             continue
@@ -696,61 +733,65 @@ def _apart(name: str, out: torch.Tensor, **inputs) -> None:
 
 def mxfp4_scale_bytes(K: int) -> int:
     """Bytes of one row's scales for K columns: one per 32, rows padded to whole 32-bit words."""
-    n = int(load_library().moe_mxfp4_scale_bytes(K))
-    if n == 0:
+    if K < 32 or K % 32 or K > 65536:
         raise ValueError(f"K = {K} is not a multiple of 32 in [32, 65536]")
-    return n
+    return (K + 127) // 128 * 4
 
 
-def _mx(name: str, codes: torch.Tensor, scales: torch.Tensor, *lead):
-    """(codes pointer, scales pointer, K) of an MXFP4 tensor [*lead, K]."""
-    if codes.dim() != len(lead) + 1:
-        raise ValueError(f"{name} codes have shape {tuple(codes.shape)}, not {lead} and K / 8")
-    K = codes.shape[-1] * 8
-    return (_dense(name + " codes", codes, torch.int32, *lead, K // 8),
-            _dense(name + " scales", scales, torch.uint8, *codes.shape[:-1], mxfp4_scale_bytes(K)), K)
+def _mx(name: str, codes: torch.Tensor, scales: torch.Tensor, dims: int):
+    """(codes pointer, scales pointer, shape with K in place of its words) of an MXFP4 tensor."""
+    shape = codes.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} codes have shape {tuple(shape)}, not {dims} dimensions")
+    lead, words = shape[:-1], shape[-1]
+    return (_dense(name, codes, torch.int32, *shape),
+            _dense(name + " scales", scales, torch.uint8, *lead, mxfp4_scale_bytes(words * 8)),
+            (*lead, words * 8))
+
+
+def _mx_out(out: tuple | None, rows: int, K: int, like: torch.Tensor):
+    """(codes, scales, their pointers) of an MXFP4 output, made here unless given."""
+    sbytes = mxfp4_scale_bytes(K)
+    if out is None:
+        codes = like.new_empty((rows, K // 8), dtype=torch.int32)
+        scales = like.new_empty((rows, sbytes), dtype=torch.uint8)
+        return codes, scales, codes.data_ptr(), scales.data_ptr()
+    codes, scales = out
+    return (codes, scales, _dense("codes", codes, torch.int32, rows, K // 8),
+            _dense("scales", scales, torch.uint8, rows, sbytes))
 
 
 def moe_mxfp4_quantize(x: torch.Tensor, out: tuple | None = None):
     """x [R, K] -> (codes int32 [R, K/8], scales uint8 [R, mxfp4_scale_bytes(K)])."""
-    ptr, dtype, stride = _matrix("x", x, None, None)
-    R, K = x.shape
-    sbytes = mxfp4_scale_bytes(K)
-    if out is None:
-        out = (torch.empty((R, K // 8), dtype=torch.int32, device=x.device),
-               torch.empty((R, sbytes), dtype=torch.uint8, device=x.device))
-    codes, scales = out
-    dev = _device_of(x=x, codes=codes, scales=scales)
-    _run("moe_mxfp4_quantize", dev, ptr, dtype, R, K, stride,
-         _dense("codes", codes, torch.int32, R, K // 8),
-         _dense("scales", scales, torch.uint8, R, sbytes))
+    ptr, dtype, stride, R, K = _matrix("x", x)
+    codes, scales, pc, ps = _mx_out(out, R, K, x)
+    _run("moe_mxfp4_quantize", _device_of(x, codes, scales), ptr, dtype, R, K, stride, pc, ps)
     return codes, scales
 
 
 def moe_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor,
                          dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None):
-    """The values of MXFP4 rows, rounded to dtype: [R, K]."""
-    pc, ps, K = _mx("x", codes, scales, None)
-    R = codes.shape[0]
+    """The values of MXFP4 rows, rounded to dtype (or out's type): [R, K]."""
+    pc, ps, (R, K) = _mx("x", codes, scales, 2)
     if out is None:
-        out = torch.empty((R, K), dtype=dtype, device=codes.device)
-    ptr, code, stride = _matrix("out", out, R, K)
-    dev = _device_of(codes=codes, scales=scales, out=out)
-    _run("moe_mxfp4_dequantize", dev, pc, ps, R, K, ptr, code, stride)
+        out = codes.new_empty((R, K), dtype=dtype)
+    ptr, code, stride = _sized("out", out, R, K)
+    _run("moe_mxfp4_dequantize", _device_of(codes, scales, out), pc, ps, R, K, ptr, code, stride)
     return out
 
 
 def _product_args(a_codes, a_scales, w_codes, w_scales, expert_offsets, row_slots, top_k):
-    pa, sa, K = _mx("a", a_codes, a_scales, None)
-    pw, sw, Kw = _mx("w", w_codes, w_scales, None, None)
+    pa, sa, (rows, K) = _mx("a", a_codes, a_scales, 2)
+    pw, sw, (E, N, Kw) = _mx("w", w_codes, w_scales, 3)
     if K != Kw:
         raise ValueError(f"a has {K} columns, w has {Kw}")
-    E = w_codes.shape[0]
-    a_rows = a_codes.shape[0]
-    rows = a_rows if row_slots is None else row_slots.shape[0]
-    po = None if expert_offsets is None else _dense("expert_offsets", expert_offsets, torch.int32, E + 1)
-    pr = None if row_slots is None else _dense("row_slots", row_slots, torch.int32, rows)
-    return (pa, sa, a_rows, pr, top_k, rows, po, E, pw, sw), rows, w_codes.shape[1], K
+    a_rows, po, pr = rows, None, None
+    if row_slots is not None:
+        rows = row_slots.numel()
+        pr = _dense("row_slots", row_slots, torch.int32, rows)
+    if expert_offsets is not None:
+        po = _dense("expert_offsets", expert_offsets, torch.int32, E + 1)
+    return (pa, sa, a_rows, pr, top_k, rows, po, E, pw, sw), rows, N, K
 
 
 def moe_mxfp4_grouped_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor,
@@ -758,15 +799,16 @@ def moe_mxfp4_grouped_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_code
                            row_slots: torch.Tensor | None = None, top_k: int = 1,
                            dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None):
     """MXFP4 rows times their expert's MXFP4 weights [E, N, K]: out [rows, N].  Rows are a's, or
-    a's row_slots[r] // top_k; without expert_offsets (E == 1) all belong to the one expert."""
+    a's row_slots[r] // top_k; without expert_offsets (E == 1) all belong to the one expert.  Rows
+    outside the experts' segments are left as they were (undefined when out is made here)."""
     args, rows, N, K = _product_args(a_codes, a_scales, w_codes, w_scales, expert_offsets,
                                      row_slots, top_k)
     if out is None:
-        out = torch.empty((rows, N), dtype=dtype, device=a_codes.device)
-    ptr, code, stride = _matrix("out", out, rows, N)
-    dev = _device_of(a_codes=a_codes, a_scales=a_scales, w_codes=w_codes, w_scales=w_scales,
-                     expert_offsets=expert_offsets, row_slots=row_slots, out=out)
-    _run("moe_mxfp4_grouped_gemm", dev, *args, N, K, ptr, code, stride)
+        out = a_codes.new_empty((rows, N), dtype=dtype)
+    ptr, code, stride = _sized("out", out, rows, N)
+    _run("moe_mxfp4_grouped_gemm",
+         _device_of(a_codes, a_scales, w_codes, w_scales, expert_offsets, row_slots, out), *args, N,
+         K, ptr, code, stride)
     return out
 
 
@@ -779,16 +821,10 @@ def moe_mxfp4_gate_up(a_codes: torch.Tensor, a_scales: torch.Tensor, w13_codes: 
                                      row_slots, top_k)
     if N % 64:
         raise ValueError(f"w13 has {N} rows per expert, not a multiple of 64")
-    I = N // 2
-    sbytes = mxfp4_scale_bytes(I)
-    if out is None:
-        out = (torch.empty((rows, I // 8), dtype=torch.int32, device=a_codes.device),
-               torch.empty((rows, sbytes), dtype=torch.uint8, device=a_codes.device))
-    codes, scales = out
-    dev = _device_of(a_codes=a_codes, a_scales=a_scales, w13_codes=w13_codes, w13_scales=w13_scales,
-                     expert_offsets=expert_offsets, row_slots=row_slots, codes=codes, scales=scales)
-    _run("moe_mxfp4_gate_up", dev, *args, I, H, _dense("codes", codes, torch.int32, rows, I // 8),
-         _dense("scales", scales, torch.uint8, rows, sbytes))
+    codes, scales, pc, ps = _mx_out(out, rows, N // 2, a_codes)
+    _run("moe_mxfp4_gate_up",
+         _device_of(a_codes, a_scales, w13_codes, w13_scales, expert_offsets, row_slots, codes,
+                    scales), *args, N // 2, H, pc, ps)
     return codes, scales
 
 
@@ -800,23 +836,24 @@ def moe_mxfp4_layer_forward(logits: torch.Tensor, x: torch.Tensor, top_k: int, w
                             workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
     """The routed-expert layer on MXFP4 experts: logits fp32 [T, E], x [T, H] -> out [T, H] of
     x's type.  w: w13_codes, w13_scales [E, 2I, H] and w2_codes, w2_scales [E, H, I]."""
-    T, E = logits.shape
-    pw13, sw13, H = _mx("w13", w["w13_codes"], w["w13_scales"], E, None)
-    pw2, sw2, I = _mx("w2", w["w2_codes"], w["w2_scales"], E, H)
-    if w["w13_codes"].shape[1] != 2 * I:
-        raise ValueError(f"w13 has {w['w13_codes'].shape[1]} rows per expert, w2 has {I} columns")
-    if x.dtype not in _DTYPE:
-        raise ValueError(f"x is {x.dtype}, not float32, float16 or bfloat16")
+    w13, w13_s, w2, w2_s = w["w13_codes"], w["w13_scales"], w["w2_codes"], w["w2_scales"]
+    pw13, sw13, (E, N, H) = _mx("w13", w13, w13_s, 3)
+    pw2, sw2, (E2, H2, I) = _mx("w2", w2, w2_s, 3)
+    if (E2, H2, 2 * I) != (E, H, N):
+        raise ValueError(f"w13 is {(E, N, H)}, w2 is {(E2, H2, I)}: not [E, 2I, H] and [E, H, I]")
+    dtype = x.dtype
+    code = _DTYPE.get(dtype)
+    if code is None:
+        raise ValueError(f"x is {dtype}, not float32, float16 or bfloat16")
+    T = x.shape[0]
+    px, pl = _dense("x", x, dtype, T, H), _dense("logits", logits, torch.float32, T, E)
     if out is None:
-        out = torch.empty((T, H), dtype=x.dtype, device=x.device)
-    need = mxfp4_layer_workspace_bytes(T, top_k, E, H, I)
+        out = x.new_empty((T, H))
     if workspace is None:
-        workspace = _workspace(need, x.device)
-    dev = _device_of(logits=logits, x=x, out=out, workspace=workspace, **w)
-    _run("moe_mxfp4_layer_forward", dev, _dense("logits", logits, torch.float32, T, E),
-         _dense("x", x, x.dtype, T, H), _DTYPE[x.dtype], T, E, top_k, pw13, sw13, pw2, sw2, H, I,
-         _dense("out", out, x.dtype, T, H), _dense("workspace", workspace, torch.uint8, None),
-         workspace.numel())
+        workspace = x.new_empty(mxfp4_layer_workspace_bytes(T, top_k, E, H, I), dtype=torch.uint8)
+    _run("moe_mxfp4_layer_forward", _device_of(logits, x, w13, w13_s, w2, w2_s, out, workspace), pl,
+         px, code, T, E, top_k, pw13, sw13, pw2, sw2, H, I, _dense("out", out, dtype, T, H),
+         *_bytes("workspace", workspace))
     return out
 
 
@@ -831,31 +868,43 @@ def moe_permute_masked(topk_ids: torch.Tensor, E: int, first_expert: int = 0,
     if topk_ids.dim() != 2:
         raise ValueError(f"topk_ids has shape {tuple(topk_ids.shape)}, not [T, top_k]")
     T, k = topk_ids.shape
-    dev, S = topk_ids.device, T * k
+    S = T * k
     if out is None:
-        out = {name: torch.empty(n, dtype=torch.int32, device=dev) for name, n in (
+        out = {name: topk_ids.new_empty(n, dtype=torch.int32) for name, n in (
             ("expert_offsets", E + 1), ("sorted_slots", S), ("slot_rows", S),
             ("active_experts", E), ("num_active", 1))}
         if T == 0:  # the call writes nothing then
             for name, fill in (("expert_offsets", 0), ("active_experts", -1), ("num_active", 0)):
                 out[name].fill_(fill)
     if workspace is None:
-        workspace = _workspace(permute_masked_workspace_bytes(T, k, E), dev)
-    _device_of(topk_ids=topk_ids, workspace=workspace, **out)
-    _run("moe_permute_masked", dev, _dense("topk_ids", topk_ids, torch.int32, T, k), T, k,
-         first_expert, E, _dense("expert_offsets", out["expert_offsets"], torch.int32, E + 1),
-         _dense("sorted_slots", out["sorted_slots"], torch.int32, S),
-         _dense("slot_rows", out["slot_rows"], torch.int32, S),
-         _dense("active_experts", out["active_experts"], torch.int32, E),
-         _dense("num_active", out["num_active"], torch.int32, 1),
-         _dense("workspace", workspace, torch.uint8, None), workspace.numel())
+        need = permute_masked_workspace_bytes(T, k, E)
+        if need:
+            workspace = topk_ids.new_empty(need, dtype=torch.uint8)
+    offsets, slots, rows = out["expert_offsets"], out["sorted_slots"], out["slot_rows"]
+    active, count = out["active_experts"], out["num_active"]
+    _run("moe_permute_masked", _device_of(topk_ids, offsets, slots, rows, active, count, workspace),
+         _dense("topk_ids", topk_ids, torch.int32, T, k), T, k, first_expert, E,
+         _dense("expert_offsets", offsets, torch.int32, E + 1),
+         _dense("sorted_slots", slots, torch.int32, S), _dense("slot_rows", rows, torch.int32, S),
+         _dense("active_experts", active, torch.int32, E),
+         _dense("num_active", count, torch.int32, 1), *_bytes("workspace", workspace))
     return out
 
 
-def _tokens(slot_rows: torch.Tensor, top_k: int) -> int:
-    if top_k < 1 or slot_rows.dim() != 1 or slot_rows.shape[0] % top_k:
+def _slots(slot_rows: torch.Tensor, top_k: int):
+    """(pointer, tokens) of slot_rows [T * top_k]."""
+    S = slot_rows.numel()
+    if top_k < 1 or S % top_k:
         raise ValueError(f"slot_rows has shape {tuple(slot_rows.shape)}, not [T * {top_k}]")
-    return slot_rows.shape[0] // top_k
+    return _dense("slot_rows", slot_rows, torch.int32, S), S // top_k
+
+
+def _weights(topk_weights: torch.Tensor):
+    """(pointer, T, top_k) of router weights fp32 [T, top_k]."""
+    if topk_weights.dim() != 2:
+        raise ValueError(f"topk_weights has shape {tuple(topk_weights.shape)}, not [T, top_k]")
+    T, k = topk_weights.shape
+    return _dense("topk_weights", topk_weights, torch.float32, T, k), T, k
 
 
 def moe_dispatch(x: torch.Tensor, slot_rows: torch.Tensor, top_k: int,
@@ -863,36 +912,30 @@ def moe_dispatch(x: torch.Tensor, slot_rows: torch.Tensor, top_k: int,
     """Token rows to expert order: out[slot_rows[s]] = x[s // top_k].  out has T * top_k rows, or
     any number when given; rows that no slot points at are left as they were (zero when out is
     made here)."""
-    T = _tokens(slot_rows, top_k)
-    px, dtype, sx = _matrix("x", x, T, None)
-    H = x.shape[1]
+    pr, T = _slots(slot_rows, top_k)
+    px, dtype, sx, rows_x, H = _matrix("x", x)
+    if rows_x != T:
+        raise ValueError(f"x has {rows_x} rows, slot_rows {T} tokens")
     if out is None:
-        out = torch.zeros((T * top_k, H), dtype=x.dtype, device=x.device)
-    if out.dtype != x.dtype:
-        raise ValueError(f"out is {out.dtype}, x is {x.dtype}")
-    po, _, so = _matrix("out", out, None, H)
-    dev = _device_of(x=x, slot_rows=slot_rows, out=out)
+        out = x.new_zeros((T * top_k, H))
+    rows = out.shape[0]
+    po, _, so = _sized("out", out, rows, H, dtype)
     _apart("out", out, x=x)
-    _run("moe_dispatch", dev, px, dtype, T, top_k, H, sx,
-         _dense("slot_rows", slot_rows, torch.int32, T * top_k), out.shape[0], po, so)
+    _run("moe_dispatch", _device_of(x, slot_rows, out), px, dtype, T, top_k, H, sx, pr, rows, po, so)
     return out
 
 
 def moe_dispatch_backward(grad_sorted: torch.Tensor, slot_rows: torch.Tensor, top_k: int,
                           out: torch.Tensor | None = None) -> torch.Tensor:
     """moe_dispatch's gradient: grad_x [T, H], the sum of a token's rows (zeros without one)."""
-    T = _tokens(slot_rows, top_k)
-    pg, dtype, sg = _matrix("grad_sorted", grad_sorted, None, None)
-    rows, H = grad_sorted.shape
+    pr, T = _slots(slot_rows, top_k)
+    pg, dtype, sg, rows, H = _matrix("grad_sorted", grad_sorted)
     if out is None:
-        out = torch.empty((T, H), dtype=grad_sorted.dtype, device=grad_sorted.device)
-    if out.dtype != grad_sorted.dtype:
-        raise ValueError(f"out is {out.dtype}, grad_sorted is {grad_sorted.dtype}")
-    po, _, so = _matrix("out", out, T, H)
-    dev = _device_of(grad_sorted=grad_sorted, slot_rows=slot_rows, out=out)
+        out = grad_sorted.new_empty((T, H))
+    po, _, so = _sized("out", out, T, H, dtype)
     _apart("out", out, grad_sorted=grad_sorted)
-    _run("moe_dispatch_backward", dev, pg, dtype, T, top_k, H, sg,
-         _dense("slot_rows", slot_rows, torch.int32, T * top_k), rows, po, so)
+    _run("moe_dispatch_backward", _device_of(grad_sorted, slot_rows, out), pg, dtype, T, top_k, H,
+         sg, pr, rows, po, so)
     return out
 
 
@@ -900,19 +943,14 @@ def moe_combine_masked(y_sorted: torch.Tensor, topk_weights: torch.Tensor, slot_
                        dtype: torch.dtype | None = None, out: torch.Tensor | None = None):
     """The router-weighted sum of a token's rows, dropped slots left out: out [T, H] of `dtype`
     (default: y_sorted's)."""
-    if topk_weights.dim() != 2:
-        raise ValueError(f"topk_weights has shape {tuple(topk_weights.shape)}, not [T, top_k]")
-    T, k = topk_weights.shape
-    py, y_code, sy = _matrix("y_sorted", y_sorted, None, None)
-    rows, H = y_sorted.shape
+    pw, T, k = _weights(topk_weights)
+    py, y_code, sy, rows, H = _matrix("y_sorted", y_sorted)
     if out is None:
-        out = torch.empty((T, H), dtype=dtype or y_sorted.dtype, device=y_sorted.device)
-    po, o_code, so = _matrix("out", out, T, H)
-    dev = _device_of(y_sorted=y_sorted, topk_weights=topk_weights, slot_rows=slot_rows, out=out)
+        out = y_sorted.new_empty((T, H), dtype=dtype)
+    po, o_code, so = _sized("out", out, T, H)
     _apart("out", out, y_sorted=y_sorted)
-    _run("moe_combine_masked", dev, py, y_code, T, k, H, sy,
-         _dense("topk_weights", topk_weights, torch.float32, T, k),
-         _dense("slot_rows", slot_rows, torch.int32, T * k), rows, po, o_code, so)
+    _run("moe_combine_masked", _device_of(y_sorted, topk_weights, slot_rows, out), py, y_code, T, k,
+         H, sy, pw, _dense("slot_rows", slot_rows, torch.int32, T * k), rows, po, o_code, so)
     return out
 
 
@@ -921,24 +959,17 @@ def moe_combine_backward(grad_out: torch.Tensor, y_sorted: torch.Tensor,
                          out: torch.Tensor | None = None, grad_weights: torch.Tensor | None = None):
     """moe_combine_masked's gradients: (grad_y of y_sorted's type and shape, grad_weights fp32
     [T, top_k]).  Rows of grad_y that no slot points at are left as they were (zero when made here)."""
-    if topk_weights.dim() != 2:
-        raise ValueError(f"topk_weights has shape {tuple(topk_weights.shape)}, not [T, top_k]")
-    T, k = topk_weights.shape
-    py, y_code, sy = _matrix("y_sorted", y_sorted, None, None)
-    rows, H = y_sorted.shape
-    pg, g_code, sg = _matrix("grad_out", grad_out, T, H)
+    pw, T, k = _weights(topk_weights)
+    py, y_code, sy, rows, H = _matrix("y_sorted", y_sorted)
+    pg, g_code, sg = _sized("grad_out", grad_out, T, H)
     if out is None:
-        out = torch.zeros((rows, H), dtype=y_sorted.dtype, device=y_sorted.device)
-    if out.dtype != y_sorted.dtype:
-        raise ValueError(f"out is {out.dtype}, y_sorted is {y_sorted.dtype}")
-    po, _, so = _matrix("out", out, rows, H)
+        out = y_sorted.new_zeros((rows, H))
+    po, _, so = _sized("out", out, rows, H, y_code)
     if grad_weights is None:
-        grad_weights = torch.empty((T, k), dtype=torch.float32, device=y_sorted.device)
-    dev = _device_of(grad_out=grad_out, y_sorted=y_sorted, topk_weights=topk_weights,
-                     slot_rows=slot_rows, out=out, grad_weights=grad_weights)
+        grad_weights = topk_weights.new_empty((T, k))
     _apart("out", out, y_sorted=y_sorted, grad_out=grad_out)
-    _run("moe_combine_backward", dev, pg, g_code, sg, py, y_code, sy,
-         _dense("topk_weights", topk_weights, torch.float32, T, k),
-         _dense("slot_rows", slot_rows, torch.int32, T * k), T, k, H, rows, po, so,
+    _run("moe_combine_backward",
+         _device_of(grad_out, y_sorted, topk_weights, slot_rows, out, grad_weights), pg, g_code, sg,
+         py, y_code, sy, pw, _dense("slot_rows", slot_rows, torch.int32, T * k), T, k, H, rows, po, so,
          _dense("grad_weights", grad_weights, torch.float32, T, k))
     return out, grad_weights
