@@ -153,32 +153,41 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxGemmArgs p, int n_tile
 
 // ------------------------------------------------------------------- tiles --
 // A workgroup takes tiles of BW weight rows x BT tokens, one after the other,
-// and walks K in chunks of 256 values (128 bytes of codes and 8 of scales per
-// row).  Chunks go from memory straight to LDS (no registers in between) in a
-// ring of STAGES: the next one is requested as soon as its place is free, one
-// barrier per chunk, and the sequence of chunks runs on over the tiles, so the
-// loads of a tile are on their way while the one before is multiplied and
-// stored.  In LDS a row's eight 16-byte blocks are stored with their number
-// xor (row mod 8), so the 16-byte reads of 8 neighbouring rows meet different
-// banks.
+// and walks K in chunks of CB 32-value blocks (16 CB bytes of codes and CB of
+// scales per row).  Chunks go from memory straight to LDS (no registers in
+// between) in a ring of STAGES: the next one is requested as soon as its place
+// is free, one barrier per chunk, and the sequence of chunks runs on over the
+// tiles, so the loads of a tile are on their way while the one before is
+// multiplied and stored.  In LDS a row's blocks are stored with their number
+// xor a few bits of the row's, so that the 16-byte reads of 8 neighbouring rows
+// meet different banks.
 //
 // Tokens behind a segment and weight rows behind N leave what LDS holds, or
 // rows that follow: each result depends on its own row and token only, and
 // theirs are not stored.
 template <int BW_, int BT_, int WW_, int WT_, int STAGES_>
 struct TileShape {
-  static constexpr int BW = BW_, BT = BT_, WW = WW_, WT = WT_, STAGES = STAGES_;
+  static constexpr int BW = BW_, BT = BT_, WW = WW_, WT = WT_, CB = 8, STAGES = STAGES_;
   static constexpr int kWaves = WW * WT;
   static constexpr int NW = BW / 32 / WW, NT = BT / 32 / WT;  // 32 x 32 results per wave
-  static constexpr int kCodes = (BW + BT) * 128;
-  static constexpr int kStage = kCodes + (BW + BT) * 8;
-  static constexpr int kLoadW = BW / 8 / kWaves, kLoadT = BT / 8 / kWaves;
-  static constexpr int kScaleW = (BW / 32 + kWaves - 1) / kWaves;
-  static constexpr int kScaleT = (BT / 32 + kWaves - 1) / kWaves;
+  static constexpr int kRow = 16 * CB;                        // bytes of codes per row and chunk
+  static constexpr int kCodes = (BW + BT) * kRow;
+  static constexpr int kStage = kCodes + (BW + BT) * CB;
+  static constexpr int kRowsPerLoad = 1024 / kRow;            // a wave's load of 16 bytes per lane
+  static constexpr int kLoadW = BW / kRowsPerLoad / kWaves, kLoadT = BT / kRowsPerLoad / kWaves;
+  static constexpr int kSetRows = 256 / CB;                   // rows per load of scale words
+  static constexpr int kSetsW = BW / kSetRows, kSetsT = (BT + kSetRows - 1) / kSetRows;
+  static constexpr int kScaleW = (kSetsW + kWaves - 1) / kWaves;
+  static constexpr int kScaleT = (kSetsT + kWaves - 1) / kWaves;
   static constexpr int kLoads = kLoadW + kLoadT + kScaleW + kScaleT;  // per wave and chunk
-  static constexpr int kPerCu = static_cast<int>(kGfx950LdsBytes) / (STAGES * kStage);
-  static_assert(STAGES * kStage <= static_cast<int>(kGfx950LdsBytes), "the ring fits in LDS");
-  static_assert(kLoadW * kWaves * 8 == BW && kLoadT * kWaves * 8 == BT, "loads divide evenly");
+  static constexpr int kTurn = 128, kScratch = 32 * kTurn;    // results turn per wave, below
+  static constexpr int kLds = STAGES * kStage + static_cast<int>(sizeof(TileTable));
+  static constexpr int kPerCu = static_cast<int>(kGfx950LdsBytes) / kLds;
+  static_assert(kLds <= static_cast<int>(kGfx950LdsBytes), "the ring fits in LDS");
+  static_assert(kLoadW * kWaves * kRowsPerLoad == BW && kLoadT * kWaves * kRowsPerLoad == BT &&
+                    kSetsW * kSetRows == BW && (BT % kSetRows == 0),
+                "loads divide evenly");
+  static_assert(kWaves * kScratch <= kStage, "results turn inside one stage");
 };
 
 // Loads from memory straight to LDS, 16 or 4 bytes per lane: from the lane's
@@ -246,8 +255,9 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
   // (the workgroups of equal index mod 8) a contiguous run of them: the tiles
   // that run together share weight rows and tokens in its L2.
   constexpr int kGroupTiles = 4;
-  const Tiles tiles = count_tiles(p.offsets, p.E, p.rows, S::BT);
-  const int all = tiles.total * n_tiles;
+  __shared__ TileTable table;
+  const int total = keep_tiles(count_tiles(p.offsets, p.E, p.rows, S::BT), table);
+  const int all = total * n_tiles;
   const int run = (all + 7) >> 3;
   const int run0 = (blockIdx.x & 7) * run;
   const int run_n = min(run, all - run0);
@@ -261,20 +271,22 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
     const int tile = run0 + first_tile + j * step;
     const int grp = tile / (kGroupTiles * n_tiles);
     const int in = tile - grp * kGroupTiles * n_tiles;
-    const int gm = min(kGroupTiles, tiles.total - grp * kGroupTiles);
+    const int gm = min(kGroupTiles, total - grp * kGroupTiles);
     Tile t{in / gm, 0, 0, 0};
-    find_tile(tiles, grp * kGroupTiles + in - t.nt * gm, t.e, t.r0, t.r1);
+    find_tile(kept_tiles(table, p.offsets, p.E, p.rows, S::BT, total),
+              grp * kGroupTiles + in - t.nt * gm, t.e, t.r0, t.r1);
     return t;
   };
 
-  const int blocks = p.K / 32, chunks = (blocks + 7) / 8;
+  const int blocks = p.K / 32, chunks = (blocks + S::CB - 1) / S::CB;
   const int row_bytes = p.K / 2, sbytes = mx_scale_bytes(p.K);
   const int I = p.N / 2;
 
   // ---- loads: the tile and chunk that are requested next
   Descriptor rw, rws, ra, ras;
   uint32_t at_w[S::kLoadW], at_t[S::kLoadT], at_ws[S::kScaleW], at_ts[S::kScaleT];
-  // the 32 rows whose scales this wave loads; spare waves repeat a load
+  auto swizzle = [](int row) { return row & 7; };
+  // the set of rows whose scales this wave loads; spare waves repeat a load
   auto scale_set = [&](int i, int sets) { return (i * S::kWaves + wave) % sets; };
   auto aim = [&](const Tile& t) {
     rw = descriptor(p.w_codes + static_cast<int64_t>(t.e) * p.N * row_bytes,
@@ -300,22 +312,24 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
       const int64_t a = a_row(p, t.r0 + tr);
       return a < 0 ? kOutOfRange : static_cast<uint32_t>(a) * bytes;
     };
+    const int in_row = lane / S::CB, at = lane % S::CB;  // this lane's part of a load
 #pragma unroll
     for (int i = 0; i < S::kLoadW; ++i) {
-      const int rr = (i * S::kWaves + wave) * 8 + (lane >> 3);
-      at_w[i] = w_row(rr) * row_bytes + ((lane ^ rr) & 7) * 16;
+      const int rr = (i * S::kWaves + wave) * S::kRowsPerLoad + in_row;
+      at_w[i] = w_row(rr) * row_bytes + (at ^ swizzle(rr)) * 16;
     }
 #pragma unroll
     for (int i = 0; i < S::kLoadT; ++i) {
-      const int tr = (i * S::kWaves + wave) * 8 + (lane >> 3);
-      at_t[i] = t_at(tr, row_bytes) + ((lane ^ tr) & 7) * 16;
+      const int tr = (i * S::kWaves + wave) * S::kRowsPerLoad + in_row;
+      at_t[i] = t_at(tr, row_bytes) + (at ^ swizzle(tr)) * 16;
     }
+    const int set_row = lane / (S::CB / 4), word = lane % (S::CB / 4) * 4;
 #pragma unroll
     for (int i = 0; i < S::kScaleW; ++i)
-      at_ws[i] = w_row(scale_set(i, S::BW / 32) * 32 + (lane >> 1)) * sbytes + (lane & 1) * 4;
+      at_ws[i] = w_row(scale_set(i, S::kSetsW) * S::kSetRows + set_row) * sbytes + word;
 #pragma unroll
     for (int i = 0; i < S::kScaleT; ++i)
-      at_ts[i] = t_at(scale_set(i, S::BT / 32) * 32 + (lane >> 1), sbytes) + (lane & 1) * 4;
+      at_ts[i] = t_at(scale_set(i, S::kSetsT) * S::kSetRows + set_row, sbytes) + word;
   };
   int load_tile = 0, load_chunk = 0;
   uint32_t load_at = lds_address(ring);
@@ -326,114 +340,163 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
 #pragma unroll
     for (int i = 0; i < S::kLoadW; ++i) {
       load16_to_lds(rw, load_at + (i * S::kWaves + wave) * 1024, at_w[i]);
-      at_w[i] += 128;
+      at_w[i] += S::kRow;
     }
 #pragma unroll
     for (int i = 0; i < S::kLoadT; ++i) {
-      load16_to_lds(ra, load_at + S::BW * 128 + (i * S::kWaves + wave) * 1024, at_t[i]);
-      at_t[i] += 128;
+      load16_to_lds(ra, load_at + S::BW * S::kRow + (i * S::kWaves + wave) * 1024, at_t[i]);
+      at_t[i] += S::kRow;
     }
 #pragma unroll
     for (int i = 0; i < S::kScaleW; ++i) {
-      load4_to_lds(rws, load_at + S::kCodes + scale_set(i, S::BW / 32) * 256, at_ws[i]);
-      at_ws[i] += 8;
+      load4_to_lds(rws, load_at + S::kCodes + scale_set(i, S::kSetsW) * 256, at_ws[i]);
+      at_ws[i] += S::CB;
     }
 #pragma unroll
     for (int i = 0; i < S::kScaleT; ++i) {
-      load4_to_lds(ras, load_at + S::kCodes + S::BW * 8 + scale_set(i, S::BT / 32) * 256, at_ts[i]);
-      at_ts[i] += 8;
+      load4_to_lds(ras, load_at + S::kCodes + S::BW * S::CB + scale_set(i, S::kSetsT) * 256,
+                   at_ts[i]);
+      at_ts[i] += S::CB;
     }
-    load_at += S::kStage;
-    if (load_at == ring_at + S::STAGES * S::kStage) load_at = ring_at;
-    if (++load_chunk == chunks) {
-      load_chunk = 0;
-      if (++load_tile < mine)
-        aim(locate(load_tile));
-      else
-        rw.d[2] = rws.d[2] = ra.d[2] = ras.d[2] = 0;
-    }
+    load_at = load_at == ring_at + (S::STAGES - 1) * S::kStage ? ring_at : load_at + S::kStage;
+    ++load_chunk;
+  };
+  // Aims at the next tile when all of this one's chunks are requested.  Called
+  // apart from load_next, which so has no branches and stays one block with the
+  // products around it.
+  auto aim_next = [&]() {
+    if (load_chunk < chunks) return;
+    load_chunk = 0;
+    if (++load_tile < mine)
+      aim(locate(load_tile));
+    else
+      rw.d[2] = rws.d[2] = ra.d[2] = ras.d[2] = 0;
   };
 
   // ---- products
   const int col = lane & 31, g = lane >> 5;
   f32x16 acc[S::NW][S::NT];
   // Step s multiplies blocks 2s and 2s + 1 of the chunk, lane half g taking
-  // block 2s + g; its scale byte is byte 2s + g of the row's eight.  The places
-  // of the fragments of one side differ by whole 32 rows (4096 bytes).
-  uint32_t at_w4[4], at_t4[4];
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const uint32_t in_rows = col * 128 + (((2 * s + g) ^ col) & 7) * 16;
-    at_w4[s] = ww * S::NW * 4096 + in_rows;
-    at_t4[s] = S::BW * 128 + wt * S::NT * 4096 + in_rows;
-  }
-  const uint32_t at_w1 = S::kCodes + (ww * S::NW * 32 + col) * 8;
-  const uint32_t at_t1 = S::kCodes + (S::BW + wt * S::NT * 32 + col) * 8;
+  // block 2s + g; its scale byte is byte 2s + g of the row's.  The place of
+  // block 2s + g is block g's xor 32 s; the fragments of one side differ by
+  // whole 32 rows.
+  const uint32_t in_rows = col * S::kRow + (g ^ swizzle(col)) * 16;
+  const uint32_t at_wf = ww * S::NW * 32 * S::kRow + in_rows;
+  const uint32_t at_tf = (S::BW + wt * S::NT * 32) * S::kRow + in_rows;
+  const uint32_t at_w1 = S::kCodes + (ww * S::NW * 32 + col) * S::CB;
+  const uint32_t at_t1 = S::kCodes + (S::BW + wt * S::NT * 32 + col) * S::CB;
   auto compute = [&](const uint8_t* st) {
-    auto frag = [&](uint32_t at, int i) {
-      return *reinterpret_cast<const dwords4*>(st + at + i * 4096);
+    struct Step {
+      dwords4 w[S::NW], t[S::NT];
+    };
+    struct Scales {
+      uint32_t v[S::CB / 4];
+    };
+    auto read = [&](int s) {
+      Step f;
+#pragma unroll
+      for (int i = 0; i < S::NT; ++i)
+        f.t[i] = *reinterpret_cast<const dwords4*>(st + (at_tf ^ (32 * s)) + i * 32 * S::kRow);
+#pragma unroll
+      for (int i = 0; i < S::NW; ++i)
+        f.w[i] = *reinterpret_cast<const dwords4*>(st + (at_wf ^ (32 * s)) + i * 32 * S::kRow);
+      return f;
     };
     auto scale = [&](uint32_t at, int i) {
-      uint2 v = *reinterpret_cast<const uint2*>(st + at + i * 256);
-      v.x >>= 8 * g;
-      v.y >>= 8 * g;
+      Scales v = *reinterpret_cast<const Scales*>(st + at + i * 32 * S::CB);
+#pragma unroll
+      for (int q = 0; q < S::CB / 4; ++q) v.v[q] >>= 8 * g;
       return v;
     };
-    uint2 ws[S::NW], ts[S::NT];
+    Scales ws[S::NW], ts[S::NT];
 #pragma unroll
     for (int i = 0; i < S::NW; ++i) ws[i] = scale(at_w1, i);
 #pragma unroll
     for (int i = 0; i < S::NT; ++i) ts[i] = scale(at_t1, i);
-    auto multiply = [&](auto sc) {
+    auto multiply = [&](const Step& f, auto sc) {
       constexpr int s = decltype(sc)::value;
-      dwords4 w[S::NW], t[S::NT];
-#pragma unroll
-      for (int i = 0; i < S::NW; ++i) w[i] = frag(at_w4[s], i);
-#pragma unroll
-      for (int i = 0; i < S::NT; ++i) t[i] = frag(at_t4[s], i);
 #pragma unroll
       for (int i = 0; i < S::NW; ++i)
 #pragma unroll
         for (int j = 0; j < S::NT; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              operand(w[i]), operand(t[j]), acc[i][j], kFp4, kFp4, 2 * (s & 1),
-              s < 2 ? ws[i].x : ws[i].y, 2 * (s & 1), s < 2 ? ts[j].x : ts[j].y);
+              operand(f.w[i]), operand(f.t[j]), acc[i][j], kFp4, kFp4, 2 * (s & 1), ws[i].v[s / 2],
+              2 * (s & 1), ts[j].v[s / 2]);
     };
-    multiply(std::integral_constant<int, 0>{});
-    multiply(std::integral_constant<int, 1>{});
-    multiply(std::integral_constant<int, 2>{});
-    multiply(std::integral_constant<int, 3>{});
+    // the next step's reads go ahead of a step's products
+    Step f0 = read(0), f1 = read(1);
+    multiply(f0, std::integral_constant<int, 0>{});
+    f0 = read(2);
+    multiply(f1, std::integral_constant<int, 1>{});
+    f1 = read(3);
+    multiply(f0, std::integral_constant<int, 2>{});
+    multiply(f1, std::integral_constant<int, 3>{});
   };
-  // A last chunk of fewer than 8 blocks: the others become zeros of scale 1.
+  // A last chunk of fewer blocks: the others become zeros of scale 1.
   auto cut = [&](uint8_t* st, int live) {
-    for (int i = threadIdx.x; i < (S::BW + S::BT) * 8; i += 64 * S::kWaves) {
-      const int row = i >> 3, b = i & 7;
+    for (int i = threadIdx.x; i < (S::BW + S::BT) * S::CB; i += 64 * S::kWaves) {
+      const int row = i / S::CB, b = i % S::CB;
       if (b < live) continue;
-      *reinterpret_cast<dwords4*>(st + row * 128 + ((b ^ row) & 7) * 16) = dwords4{};
-      st[S::kCodes + row * 8 + b] = 127;
+      *reinterpret_cast<dwords4*>(st + row * S::kRow + (b ^ swizzle(row)) * 16) = dwords4{};
+      st[S::kCodes + row * S::CB + b] = 127;
     }
   };
 
-  // acc[i][j][4 q + r] is weight row 32 i' + 8 q + 4 g + r of token 32 j' + col
-  auto store = [&](const Tile& tl) {
+  // acc[i][j][4 q + r] is weight row 32 i' + 8 q + 4 g + r of token 32 j' + col.
+  // Plain results turn in LDS, 32 tokens x kTurn bytes of them at a time, so
+  // that eight neighbouring lanes store that many contiguous bytes of a token (straight from the registers a store's neighbouring lanes lie in
+  // different rows, which took as long as half the products).  `turn` is this
+  // wave's place; a token's 16-byte slots are stored with their number xor a few
+  // bits of the token's.
+  auto store = [&](const Tile& tl, uint8_t* turn) {
 #pragma unroll
     for (int j = 0; j < S::NT; ++j) {
-      const int row = tl.r0 + (wt * S::NT + j) * 32 + col;
-      if (row >= tl.r1) continue;  // both lane halves of a token alike
-      const bool none = p.row_slots != nullptr && a_row(p, row) < 0;
+      const int row0 = tl.r0 + (wt * S::NT + j) * 32;
+      const int row = row0 + col;
+      if (row0 >= tl.r1) break;
       if constexpr (!GATE_UP) {
-        auto* o = static_cast<typename TO::bits*>(p.out) + row * p.out_ld;
+        const bool none = row < tl.r1 && p.row_slots != nullptr && a_row(p, row) < 0;
+        constexpr int kCols = S::kTurn / kBytes<TO>, kSlots = S::kTurn / 16, kRows = 64 / kSlots;
+        auto slot = [](int t, int n) {
+          return (n ^ (kSlots == 8 ? t : t >> 1)) & (kSlots - 1);
+        };
 #pragma unroll
-        for (int i = 0; i < S::NW; ++i)
+        for (int c0 = 0; c0 < S::NW * 32; c0 += kCols) {
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            const int n0 = tl.nt * S::BW + (ww * S::NW + i) * 32 + 8 * q4 + 4 * g;
+          for (int e = 0; e < kCols; e += 8) {  // columns c0 + e + 4 g ... + 3
             f32x4 v;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = none ? 0.f : acc[i][j][4 * q4 + r];
-            store4<TO>(o + n0, p.N - n0, v);
+            for (int r = 0; r < 4; ++r)
+              v[r] = none ? 0.f : acc[(c0 + e) / 32][j][(c0 + e) % 32 / 2 + r];
+            const int at = (e + 4 * g) * kBytes<TO>;
+            uint8_t* to = turn + col * S::kTurn + slot(col, at >> 4) * 16;
+            if constexpr (kBytes<TO> == 4)
+              *reinterpret_cast<dwords4*>(to) = __builtin_bit_cast(dwords4, v);
+            else
+              *reinterpret_cast<dwords2*>(to + (at & 8)) = pack4<TO>(v);
           }
+          const int n0 = tl.nt * S::BW + ww * S::NW * 32 + c0 + lane % kSlots * (16 / kBytes<TO>);
+#pragma unroll
+          for (int r = 0; r < 32; r += kRows) {
+            const int t = r + lane / kSlots;
+            const dwords4 d = *reinterpret_cast<const dwords4*>(turn + t * S::kTurn +
+                                                                slot(t, lane) * 16);
+            if (row0 + t >= tl.r1) continue;
+            auto* o = static_cast<typename TO::bits*>(p.out) + (row0 + t) * p.out_ld + n0;
+            if (n0 + 16 / kBytes<TO> <= p.N) {
+              store16(o, d);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 16 / kBytes<TO>; ++x)
+                if (n0 + x < p.N)
+                  o[x] = static_cast<typename TO::bits>(
+                      kBytes<TO> == 4 ? d[x % 4] : d[x / 2] >> (16 * (x & 1)));
+            }
+          }
+        }
       } else {
+        if (row >= tl.r1) continue;  // both lane halves of a token alike
+        const bool none = p.row_slots != nullptr && a_row(p, row) < 0;
         const int sb = mx_scale_bytes(I);
 #pragma unroll
         for (int i = 0; i < S::NW; i += 2) {
@@ -471,17 +534,26 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
 
   aim(locate(0));
 #pragma unroll
-  for (int s = 0; s + 1 < S::STAGES; ++s) load_next();
+  for (int s = 0; s + 1 < S::STAGES; ++s) {
+    load_next();
+    aim_next();
+  }
   Tile now{};
   uint32_t stage = 0;
   for (int j = 0, c = 0;;) {
-    // chunk c is there when only the STAGES - 2 chunks behind it are on their
-    // way (stores among them make the wait longer, never too short)
+    // chunk c is there when only the chunks behind it are on their way (stores
+    // among them make the wait longer, never too short)
     wait_loads_and_barrier<(S::STAGES - 2) * S::kLoads>();
-    load_next();
-    if (c == 0) {
-      if (j > 0) store(now);
+    if (c == 0 && j > 0) {
+      // through the stage that is free now
+      const uint32_t free = stage == 0 ? (S::STAGES - 1) * S::kStage : stage - S::kStage;
+      store(now, ring + free + wave * S::kScratch);
       if (j == mine) break;
+      if constexpr (!GATE_UP) wait_lds_and_barrier();
+    }
+    load_next();
+    aim_next();
+    if (c == 0) {
       now = locate(j);
 #pragma unroll
       for (int i = 0; i < S::NW; ++i)
@@ -489,8 +561,8 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
         for (int t = 0; t < S::NT; ++t) acc[i][t] = f32x16{};
     }
     uint8_t* st = ring + stage;
-    if (8 * (c + 1) > blocks) {
-      cut(st, blocks - 8 * c);
+    if (S::CB * (c + 1) > blocks) {
+      cut(st, blocks - S::CB * c);
       wait_lds_and_barrier();
     }
     compute(st);

@@ -101,6 +101,36 @@ __device__ __forceinline__ Tiles count_tiles(const int* __restrict__ offsets, in
   return t;
 }
 
+// The counts kept in LDS between searches (they would hold a dozen registers
+// through a kernel's main loop): every wave writes the same values.
+struct TileTable {
+  int inc[64], sum[64], o[kHeld + 1][64];
+};
+
+__device__ __forceinline__ int keep_tiles(const Tiles& t, TileTable& table) {
+  if (t.offsets != nullptr) {
+    const int lane = threadIdx.x & 63;
+    table.inc[lane] = t.inc;
+    table.sum[lane] = t.sum;
+#pragma unroll
+    for (int i = 0; i <= kHeld; ++i) table.o[i][lane] = t.o[i];
+  }
+  return t.total;
+}
+
+__device__ __forceinline__ Tiles kept_tiles(const TileTable& table, const int* offsets, int E,
+                                            int rows, int size, int total) {
+  Tiles t{offsets, E, rows, size, (E + 63) >> 6, 0, 0, {}, total};
+  if (offsets != nullptr) {
+    const int lane = threadIdx.x & 63;
+    t.inc = table.inc[lane];
+    t.sum = table.sum[lane];
+#pragma unroll
+    for (int i = 0; i <= kHeld; ++i) t.o[i] = table.o[i][lane];
+  }
+  return t;
+}
+
 // Tile mt's expert and rows [r0, r1); false behind the last tile.
 __device__ __forceinline__ bool find_tile(const Tiles& t, int mt, int& e, int& r0, int& r1) {
   if (mt >= t.total) return false;
@@ -145,20 +175,27 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int mt, int& e, int& r
   return true;
 }
 
+typedef uint32_t dwords2 __attribute__((ext_vector_type(2)));
+
+// Four results of a 16-bit type, rounded, in two words.
+template <typename T>
+__device__ __forceinline__ dwords2 pack4(f32x4 v) {
+  dwords2 d;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    d[i] = static_cast<uint32_t>(from_float(T{}, v[2 * i])) |
+           (static_cast<uint32_t>(from_float(T{}, v[2 * i + 1])) << 16);
+  return d;
+}
+
 template <typename T>
 __device__ __forceinline__ void store4(typename T::bits* p, int n, f32x4 v) {
   if (n >= 4) {
     if constexpr (kBytes<T> == 4) {
       store16(p, __builtin_bit_cast(dwords4, v));
     } else {
-      typedef uint32_t dwords2 __attribute__((ext_vector_type(2)));
       struct __attribute__((packed, aligned(2), may_alias)) Unaligned8 { dwords2 d; };
-      dwords2 d;
-      d[0] = static_cast<uint32_t>(from_float(T{}, v[0])) |
-             (static_cast<uint32_t>(from_float(T{}, v[1])) << 16);
-      d[1] = static_cast<uint32_t>(from_float(T{}, v[2])) |
-             (static_cast<uint32_t>(from_float(T{}, v[3])) << 16);
-      reinterpret_cast<Unaligned8*>(p)->d = d;
+      reinterpret_cast<Unaligned8*>(p)->d = pack4<T>(v);
     }
   } else {
 #pragma unroll
