@@ -336,6 +336,8 @@ def _layer_steps(ops, logits, x, k, w):
 LAYERS = [  # T, E, k, H, I
     (1, 8, 2, 256, 128), (4, 8, 2, 256, 128), (9, 37, 5, 96, 160), (63, 4, 4, 160, 96),
     (130, 16, 3, 288, 64), (700, 8, 2, 128, 96), (8, 512, 10, 256, 64),
+    (2, 4, 4, 96, 32), (3, 100, 20, 544, 96), (4, 1000, 16, 1056, 224), (4, 200, 16, 64, 1088), (1, 64, 64, 128, 32),
+    (5, 8, 3, 256, 96), (4, 8, 8, 2592, 64),
 ]
 
 

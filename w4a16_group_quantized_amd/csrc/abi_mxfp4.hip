@@ -327,6 +327,28 @@ int moe_mxfp4_layer_forward(const float* logits, const void* x, int32_t dtype, i
   const MxLayerWs w = mx_layer_ws(workspace, T, top_k, E, H, I);
   if (workspace_bytes < w.total) return MOE_ERR_WORKSPACE;
   const int64_t S = T * top_k;
+  if (mx_small_ok(T, top_k, E, H, I)) {
+    MxSmallArgs a{};
+    a.logits = logits;
+    a.x = x;
+    a.dtype = dtype;
+    a.T = static_cast<int>(T);
+    a.E = E;
+    a.top_k = top_k;
+    a.H = H;
+    a.I = I;
+    a.w13_codes = reinterpret_cast<const uint8_t*>(w13_codes);
+    a.w13_scales = w13_scales;
+    a.w2_codes = reinterpret_cast<const uint8_t*>(w2_codes);
+    a.w2_scales = w2_scales;
+    a.ids = w.ids;
+    a.weights = w.weights;
+    a.act_codes = reinterpret_cast<uint8_t*>(w.act_codes);
+    a.act_scales = w.act_scales;
+    a.out = out;
+    launch_mx_small_layer(a, static_cast<hipStream_t>(stream));
+    return check_launch();
+  }
   if (int st = moe_route_permute(logits, T, E, top_k, w.ids, w.weights, w.offsets, w.sorted,
                                  w.slot_rows, w.active, w.num_active, w.perm, w.perm_bytes, stream))
     return st;

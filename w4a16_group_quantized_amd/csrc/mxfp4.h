@@ -40,6 +40,23 @@ struct MxGemmArgs {
 };
 void launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream);
 
+// The whole layer for a few tokens, in two launches (mxfp4_small.hip).
+constexpr int kMxSmallTokens = 4;
+constexpr int kMxSmallHidden = 16384;  // 4 tokens of quantised x in LDS: 34 KB
+struct MxSmallArgs {
+  const float* logits;
+  const void* x;
+  int dtype;                 // of x and out
+  int T, E, top_k, H, I;
+  const uint8_t *w13_codes, *w13_scales, *w2_codes, *w2_scales;
+  int* ids;                  // [T, top_k], written by the first launch
+  float* weights;
+  uint8_t *act_codes, *act_scales;
+  void* out;
+};
+bool mx_small_ok(int64_t T, int top_k, int E, int H, int I);
+void launch_mx_small_layer(const MxSmallArgs& p, hipStream_t stream);
+
 size_t permute_masked_workspace_bytes(int64_t T, int top_k, int E);
 void launch_permute_masked(const int* ids, int T, int top_k, int first, int E, int* offsets,
                            int* sorted_slots, int* slot_rows, int* active, int* num_active,

@@ -120,34 +120,8 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxGemmArgs p, int n_tile
     auto* o = static_cast<typename TO::bits*>(p.out) + row * p.out_ld + n0;
     store4<TO>(o, p.N - n0, acc);
   } else {
-    __shared__ float h[4][kTokens][17];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[wave][col][4 * g + i] = acc[i];
-    __syncthreads();
-    // 16 threads per token, two neighbouring columns each
-    const int t = threadIdx.x >> 4, c = (threadIdx.x & 15) * 2;
-    float a[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float gate = h[c >> 4][t][(c & 15) + q], up = h[2 + (c >> 4)][t][(c & 15) + q];
-      a[q] = silu_mul(gate, up);
-    }
-    uint32_t m = max(abs_bits(a[0]), abs_bits(a[1]));
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(m, d, 16)));
-    const uint32_t byte = mx_scale_byte(m);
-    uint32_t q = mx_pair(a[0], a[1], byte);
-    q |= __shfl_xor(q, 1, 16) << 8;  // valid in even threads
-    q |= __shfl_xor(q, 2, 16) << 16; // valid in every fourth
-    const int out_row = r0 + t;
-    if (out_row < r1) {
-      const int sb = mx_scale_bytes(I);
-      if ((threadIdx.x & 3) == 0)
-        *reinterpret_cast<uint32_t*>(p.act_codes + static_cast<int64_t>(out_row) * (I / 2) +
-                                     nt * 16 + c / 2) = q;
-      if ((threadIdx.x & 15) == 0)
-        store_scale(p.act_scales + static_cast<int64_t>(out_row) * sb, nt, I / 32, sb, byte);
-    }
+    __shared__ float h[4][16][17];
+    gate_up_epilogue(acc, h, wave, I, nt, r0, r1 - r0, p.act_codes, p.act_scales);
   }
 }
 

@@ -21,12 +21,6 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // code words per lane, their loads in flight together
 constexpr int kMaxBlocks = 1 << 20;
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  const uint32_t o = __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
-  return v > o ? v : o;
-}
-
 // SCATTER: row t goes to rows slot_rows[t top_k + j] < out_rows, j < top_k,
 // instead of row t (the rows of a token in expert order).
 template <typename T, bool SCATTER>
@@ -67,24 +61,22 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(
       m = quad_max<0xB1>(m);  // lanes 1 0 3 2
       m = quad_max<0x4E>(m);  // lanes 2 3 0 1
       const uint32_t byte = mx_scale_byte(m);
-      // 2^-e; an exact product unless it is far below the smallest code
-      const float inv = __builtin_bit_cast(float, (254u - byte) << 23);
-      uint32_t q = 0;
-      if (byte != 255) {
-        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[u][0] * inv, v[u][1] * inv, 1.f, 0);
-        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[u][2] * inv, v[u][3] * inv, 1.f, 1);
-        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[u][4] * inv, v[u][5] * inv, 1.f, 2);
-        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[u][6] * inv, v[u][7] * inv, 1.f, 3);
-      }
+      const uint32_t q = mx_word(v[u], byte);
       if (row < rows) {
         auto put = [&](int64_t to) {
           codes[to * words + c] = q;
           if ((c & 3) == 0) store_scale(scales + to * sbytes, c >> 2, words >> 2, sbytes, byte);
         };
         if constexpr (SCATTER) {
-          for (int j = 0; j < top_k; ++j) {
-            const int to = slot_rows[row * top_k + j];
-            if (static_cast<uint32_t>(to) < static_cast<uint32_t>(out_rows)) put(to);
+          // eight places at a time: their loads are in flight together
+          for (int j0 = 0; j0 < top_k; j0 += 8) {
+            int to[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              to[j] = j0 + j < top_k ? slot_rows[row * top_k + j0 + j] : -1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (static_cast<uint32_t>(to[j]) < static_cast<uint32_t>(out_rows)) put(to[j]);
           }
         } else {
           put(row);

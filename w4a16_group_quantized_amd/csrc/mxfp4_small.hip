@@ -1,0 +1,287 @@
+// The MXFP4 layer for one to four tokens in two launches.
+//
+// With so few tokens the five launches of the layer's steps (router and
+// permutation, quantisation, gate/up, down, combine) are latency: about 30 us at
+// one token of 512 experts for 26 MB of weights.  Here every workgroup does the
+// small steps for itself:
+//   gate/up  routes the tokens (one wave each) while its other waves quantise
+//            them into LDS, then takes 32 columns of I of one expert, as the
+//            streaming product does
+//   down     takes 16 columns of H of every active expert, an expert per wave,
+//            meets their rows in LDS and adds them up with the router's weights
+// The sums have the order of the separate steps' streaming kernels.
+#include "mxfp4_tile.h"
+#include "route.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxSlots = 64;  // one slot per lane
+constexpr int kMaxTokens = kMxSmallTokens;
+static_assert(kMaxTokens <= 4, "a wave per token");
+
+// The permutation of at most 64 slots, lane s holding slot s (id < 0: none):
+// the slot's row (slots ascending by expert, then by slot), and the ordinal of
+// its expert among those that hold a slot.
+struct Places {
+  int row, ordinal;
+};
+__device__ __forceinline__ Places place_slots(int id, int S) {
+  const int lane = threadIdx.x & 63;
+  int row = 0;
+  bool first = true;
+  for (int q = 0; q < S; ++q) {
+    const int other = __builtin_amdgcn_readlane(id, q);
+    row += other < id || (other == id && q < lane);
+    first &= !(other == id && q < lane);
+  }
+  unsigned long long firsts = __ballot(first && lane < S);
+  int ordinal = 0;
+  while (firsts) {
+    const int q = __builtin_ctzll(firsts);
+    firsts &= firsts - 1;
+    ordinal += __builtin_amdgcn_readlane(id, q) < id;
+  }
+  return {row, ordinal};
+}
+
+// The lanes of the n-th active expert's slots (0: there is none).
+__device__ __forceinline__ unsigned long long slots_of(const Places& p, int S, int n) {
+  return __ballot((threadIdx.x & 63) < static_cast<unsigned>(S) && p.ordinal == n);
+}
+
+// One window of 512 values of a weight row and of a token's row, as in the
+// streaming product: lane group g takes block 4 i + g at step i.
+struct WeightWindow {
+  dwords4 w[4], s;
+};
+
+struct Weights {
+  __amdgpu_buffer_rsrc_t codes, scales;
+  uint32_t at, scales_at;  // this lane's row
+  int blocks;
+};
+
+__device__ __forceinline__ void load_window(WeightWindow& b, const Weights& w, int win) {
+  const int g = (threadIdx.x & 63) >> 4, b0 = win * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int blk = b0 + 4 * i + g;
+    b.w[i] = buffer_load16(w.codes, blk < w.blocks ? w.at + blk * 16 : kOutOfRange);
+    b.s[i] = buffer_load4(w.scales, b0 + 4 * i < w.blocks ? w.scales_at + b0 + 4 * i : kOutOfRange);
+  }
+}
+
+// acc += the window's products; row(blk) gives the token's block, word(blk) the
+// scale word that holds blocks blk ... blk + 3.
+template <typename Row, typename Word>
+__device__ __forceinline__ void multiply_window(f32x4& acc, const WeightWindow& b, int win,
+                                                int blocks, Row&& row, Word&& word) {
+  const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int blk = win * 16 + 4 * i;
+    if (blk >= blocks) return;
+    const bool in = blk + g < blocks;  // blocks behind K are zeros of scale 1
+    const uint32_t sw = in ? b.s[i] >> (8 * g) : 127u;
+    const uint32_t sa = in ? word(blk) >> (8 * g) : 127u;
+    const dwords4 a = in ? row(blk + g) : dwords4{};
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(b.w[i]), operand(a), acc, kFp4,
+                                                           kFp4, 0, sw, 0, sa);
+  }
+}
+
+constexpr int kInFlight = 4;  // windows
+
+// ---- gate/up -------------------------------------------------------------------
+template <int NPL, typename TX>
+__global__ __launch_bounds__(256) void small_gate_up_kernel(MxSmallArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ int ids[kMaxSlots];
+  __shared__ float h[4][16][17];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int S = p.T * p.top_k;
+  const int n_tiles = p.I / 32;
+  const int mt = blockIdx.x / n_tiles, nt = blockIdx.x - mt * n_tiles;
+  const int blocks = p.H / 32, sbytes = mx_scale_bytes(p.H);
+  uint8_t* codes = lds;                        // [T, H / 2]
+  uint8_t* scales = lds + p.T * (p.H / 2);     // [T, sbytes]
+
+  if (wave < p.T) {
+    int id;
+    float logit, top;
+    wave_topk<NPL>(p.logits + static_cast<size_t>(wave) * p.E, p.E, p.top_k, id, logit, top);
+    const float w = wave_topk_weight(logit, top, p.top_k);
+    if (lane < p.top_k) {
+      const int s = wave * p.top_k + lane;
+      ids[s] = id;
+      if (blockIdx.x == 0) {
+        p.ids[s] = id;
+        p.weights[s] = w;
+      }
+    }
+  }
+  // the waves without a token to route quantise them; all of them when there
+  // is none
+  const int q0 = p.T < 4 ? p.T : 0;
+  if (wave >= q0) {
+    const int words = p.H / 8, total = p.T * words, step = (4 - q0) * 64;
+    for (int i0 = (wave - q0) * 64; i0 < total; i0 += step) {
+      const int i = min(i0 + lane, total - 1);  // whole blocks: total is a multiple of 4
+      const int t = i / words, c = i - t * words;
+      float v[8];
+      load8<TX>(static_cast<const typename TX::bits*>(p.x) + static_cast<size_t>(t) * p.H + 8 * c,
+                8, v);
+      uint32_t m = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) m = max(m, abs_bits(v[q]));
+      m = quad_max<0xB1>(m);
+      m = quad_max<0x4E>(m);
+      const uint32_t byte = mx_scale_byte(m);
+      if (i0 + lane < total) {
+        *reinterpret_cast<uint32_t*>(codes + t * (p.H / 2) + 4 * c) = mx_word(v, byte);
+        if ((c & 3) == 0) scales[t * sbytes + (c >> 2)] = static_cast<uint8_t>(byte);
+      }
+    }
+  }
+  __syncthreads();
+
+  const int id = lane < S ? ids[lane] : INT32_MAX;
+  const Places at = place_slots(id, S);
+  const unsigned long long mine = slots_of(at, S, mt);
+  if (mine == 0) return;  // fewer active experts: the whole workgroup alike
+  const int lead = __builtin_ctzll(mine);
+  const int e = __builtin_amdgcn_readlane(id, lead), r0 = __builtin_amdgcn_readlane(at.row, lead);
+  const int rows = __popcll(mine);
+
+  const int col = lane & 15;
+  const int n = (wave >> 1) * p.I + nt * 32 + (wave & 1) * 16 + col;
+  const int64_t N = 2 * static_cast<int64_t>(p.I);
+  const Weights w{make_rsrc(p.w13_codes + e * N * (p.H / 2), static_cast<uint32_t>(N) * (p.H / 2)),
+                  make_rsrc(p.w13_scales + e * N * sbytes, static_cast<uint32_t>(N) * sbytes),
+                  static_cast<uint32_t>(n) * (p.H / 2), static_cast<uint32_t>(n) * sbytes, blocks};
+  // the token of the tile's row `col`: its slots hold the rows in order
+  unsigned long long left = mine;
+  for (int q = 0; q < col && left; ++q) left &= left - 1;
+  const int token = left ? __builtin_ctzll(left) / p.top_k : -1;
+  const uint8_t* my_codes = codes + max(token, 0) * (p.H / 2);
+  const uint8_t* my_scales = scales + max(token, 0) * sbytes;
+  auto row = [&](int blk) {
+    return token >= 0 ? *reinterpret_cast<const dwords4*>(my_codes + blk * 16) : dwords4{};
+  };
+  auto word = [&](int blk) -> uint32_t {
+    return token >= 0 ? *reinterpret_cast<const uint32_t*>(my_scales + blk) : 0x7F7F7F7Fu;
+  };
+
+  const int windows = (blocks + 15) / 16;
+  WeightWindow b[kInFlight];
+#pragma unroll
+  for (int i = 0; i < kInFlight; ++i) load_window(b[i], w, i);
+  f32x4 acc{};
+  for (int win = 0; win < windows; win += kInFlight) {
+#pragma unroll
+    for (int i = 0; i < kInFlight; ++i) {
+      if (win + i < windows) multiply_window(acc, b[i], win + i, blocks, row, word);
+      load_window(b[i], w, win + i + kInFlight);
+    }
+  }
+  gate_up_epilogue(acc, h, wave, p.I, nt, r0, rows, p.act_codes, p.act_scales);
+}
+
+// ---- down and combine --------------------------------------------------------------
+constexpr int kDownWaves = 16;
+
+template <typename TO>
+__global__ __launch_bounds__(64 * kDownWaves) void small_down_kernel(MxSmallArgs p) {
+  __shared__ float y[kMaxSlots][17];
+  __shared__ int rows_of[kMaxSlots];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int S = p.T * p.top_k;
+  const int id = lane < S ? p.ids[lane] : INT32_MAX;
+  const Places at = place_slots(id, S);
+  if (wave == 0 && lane < S) rows_of[lane] = at.row;
+  const int blocks = p.I / 32, sbytes = mx_scale_bytes(p.I);
+  const int col = lane & 15, g = lane >> 4;
+  const int n = blockIdx.x * 16 + col;
+  const int windows = (blocks + 15) / 16;
+  for (int x = wave;; x += kDownWaves) {
+    const unsigned long long mine = slots_of(at, S, x);
+    if (mine == 0) break;
+    const int lead = __builtin_ctzll(mine);
+    const int e = __builtin_amdgcn_readlane(id, lead), r0 = __builtin_amdgcn_readlane(at.row, lead);
+    const bool live = col < __popcll(mine);
+    const int64_t r = live ? r0 + col : r0;
+    const Weights w{
+        make_rsrc(p.w2_codes + static_cast<int64_t>(e) * p.H * (p.I / 2),
+                  static_cast<uint32_t>(p.H) * (p.I / 2)),
+        make_rsrc(p.w2_scales + static_cast<int64_t>(e) * p.H * sbytes,
+                  static_cast<uint32_t>(p.H) * sbytes),
+        static_cast<uint32_t>(n) * (p.I / 2), static_cast<uint32_t>(n) * sbytes, blocks};
+    const uint8_t* my_codes = p.act_codes + r * (p.I / 2);
+    const uint8_t* my_scales = p.act_scales + r * sbytes;
+    auto row = [&](int blk) {
+      return live ? *reinterpret_cast<const dwords4*>(my_codes + blk * 16) : dwords4{};
+    };
+    auto word = [&](int blk) -> uint32_t {
+      return live ? *reinterpret_cast<const uint32_t*>(my_scales + blk) : 0x7F7F7F7Fu;
+    };
+    WeightWindow b[2];
+    load_window(b[0], w, 0);
+    load_window(b[1], w, 1);
+    f32x4 acc{};
+    for (int win = 0; win < windows; win += 2) {
+      multiply_window(acc, b[0], win, blocks, row, word);
+      load_window(b[0], w, win + 2);
+      if (win + 1 < windows) multiply_window(acc, b[1], win + 1, blocks, row, word);
+      load_window(b[1], w, win + 3);
+    }
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[r0 + col][4 * g + i] = acc[i];
+    }
+  }
+  __syncthreads();
+  const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
+  if (t < p.T) {
+    float sum = 0.f;
+    for (int j = 0; j < p.top_k; ++j)
+      sum = fmaf(p.weights[t * p.top_k + j], y[rows_of[t * p.top_k + j]][c], sum);
+    static_cast<typename TO::bits*>(p.out)[static_cast<size_t>(t) * p.H + blockIdx.x * 16 + c] =
+        from_float(TO{}, sum);
+  }
+}
+
+template <int NPL, typename TX>
+void launch_gate_up(const MxSmallArgs& p, hipStream_t stream) {
+  const int S = p.T * p.top_k, active = p.E < S ? p.E : S;
+  const size_t lds = static_cast<size_t>(p.T) * (p.H / 2 + mx_scale_bytes(p.H));
+  hipLaunchKernelGGL((small_gate_up_kernel<NPL, TX>), dim3(active * (p.I / 32)), dim3(256), lds,
+                     stream, p);
+}
+
+}  // namespace
+
+bool mx_small_ok(int64_t T, int top_k, int E, int H, int I) {
+  return T <= kMaxTokens && T * top_k <= kMaxSlots && E <= 1024 && H <= kMxSmallHidden && I > 0;
+}
+
+void launch_mx_small_layer(const MxSmallArgs& p, hipStream_t stream) {
+  with_dtype(p.dtype, [&](auto t) {
+    using T = decltype(t);
+    if (p.E <= 64)
+      launch_gate_up<1, T>(p, stream);
+    else if (p.E <= 128)
+      launch_gate_up<2, T>(p, stream);
+    else if (p.E <= 256)
+      launch_gate_up<4, T>(p, stream);
+    else if (p.E <= 512)
+      launch_gate_up<8, T>(p, stream);
+    else
+      launch_gate_up<16, T>(p, stream);
+    hipLaunchKernelGGL(small_down_kernel<T>, dim3(p.H / 16), dim3(64 * kDownWaves), 0, stream, p);
+  });
+}
+
+}  // namespace moe

@@ -232,6 +232,25 @@ __device__ __forceinline__ uint32_t mx_pair(float a, float b, uint32_t byte) {
   if (byte == 255) return 0;
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, a * inv, b * inv, 1.f, 0) & 0xFFu;
 }
+// All eight codes of a word (v as loaded, byte their block's).
+__device__ __forceinline__ uint32_t mx_word(const float (&v)[8], uint32_t byte) {
+  // 2^-e; an exact product unless it is far below the smallest code
+  const float inv = __builtin_bit_cast(float, (254u - byte) << 23);
+  uint32_t q = 0;
+  if (byte != 255) {
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0] * inv, v[1] * inv, 1.f, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2] * inv, v[3] * inv, 1.f, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4] * inv, v[5] * inv, 1.f, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6] * inv, v[7] * inv, 1.f, 3);
+  }
+  return q;
+}
+// Maximum with a neighbour in the quad (CTRL: quad permutation).
+template <int CTRL>
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  const uint32_t o = __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+  return v > o ? v : o;
+}
 // Block `blk`'s scale of a row of `blocks`; the last one also sets the row's
 // padding, which stands for 1.
 __device__ __forceinline__ void store_scale(uint8_t* row, int blk, int blocks, int sbytes,
@@ -239,6 +258,41 @@ __device__ __forceinline__ void store_scale(uint8_t* row, int blk, int blocks, i
   row[blk] = static_cast<uint8_t>(byte);
   if (blk + 1 == blocks)
     for (int p = blocks; p < sbytes; ++p) row[p] = 127;
+}
+
+// SiLU(gate) * up of a tile of 16 tokens x 32 columns of I, stored as MXFP4 (the
+// 32 columns are one block): waves 0 and 1 of 256 threads hold the gate's two
+// halves in acc, waves 2 and 3 the up's, lane (col, g) columns 4 g ... + 3 of
+// token col.  `h` is LDS of the workgroup.
+__device__ __forceinline__ void gate_up_epilogue(f32x4 acc, float (&h)[4][16][17], int wave, int I,
+                                                 int nt, int r0, int rows, uint8_t* act_codes,
+                                                 uint8_t* act_scales) {
+  const int col = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[wave][col][4 * g + i] = acc[i];
+  __syncthreads();
+  // 16 threads per token, two neighbouring columns each
+  const int t = threadIdx.x >> 4, c = (threadIdx.x & 15) * 2;
+  float a[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float gate = h[c >> 4][t][(c & 15) + q], up = h[2 + (c >> 4)][t][(c & 15) + q];
+    a[q] = silu_mul(gate, up);
+  }
+  uint32_t m = max(abs_bits(a[0]), abs_bits(a[1]));
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) m = max(m, static_cast<uint32_t>(__shfl_xor(m, d, 16)));
+  const uint32_t byte = mx_scale_byte(m);
+  uint32_t q = mx_pair(a[0], a[1], byte);
+  q |= __shfl_xor(q, 1, 16) << 8;   // valid in even threads
+  q |= __shfl_xor(q, 2, 16) << 16;  // valid in every fourth
+  if (t < rows) {
+    const int64_t row = r0 + t;
+    const int sb = mx_scale_bytes(I);
+    if ((threadIdx.x & 3) == 0)
+      *reinterpret_cast<uint32_t*>(act_codes + row * (I / 2) + nt * 16 + c / 2) = q;
+    if ((threadIdx.x & 15) == 0) store_scale(act_scales + row * sb, nt, I / 32, sb, byte);
+  }
 }
 
 }  // namespace moe
