@@ -357,6 +357,21 @@ def test_layer_is_its_calls_and_near_the_oracle(ops, T, E, k, H, I, dtype):
     assert np.sqrt((off ** 2).sum() / (want ** 2).sum()) <= 1e-2
 
 
+@pytest.mark.parametrize("T,E,k", [(1, 512, 10), (3, 100, 7), (4, 37, 16), (1, 1000, 60), (9, 64, 5)])
+def test_layer_with_tied_logits(ops, T, E, k):
+    """Few distinct logits, all equal ones, and a list of choices longer than a wave's lanes hold:
+    the lower expert comes first, as everywhere."""
+    rng = np.random.default_rng(E)
+    H, I = 128, 32
+    logits, x, w, w13, w2 = _layer_inputs(rng, T, E, H, I, torch.float32)
+    for step in (1.0, 100.0, 0.01):
+        tied = torch.round(logits / step) * step
+        out = ops.moe_mxfp4_layer_forward(tied, x, k, w)
+        assert torch.equal(out, _layer_steps(ops, tied, x, k, w))
+        want = ref.mx_layer(tied.cpu().numpy(), _host(x), k, w13, w2)
+        assert np.sqrt(((_host(out) - want) ** 2).sum() / (want ** 2).sum()) <= 1e-2
+
+
 def test_layer_in_a_graph_replayed(ops):
     """Replays with new inputs in the captured buffers, eager work between them."""
     rng = np.random.default_rng(8)

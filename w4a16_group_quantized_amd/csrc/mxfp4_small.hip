@@ -50,6 +50,61 @@ __device__ __forceinline__ unsigned long long slots_of(const Places& p, int S, i
   return __ballot((threadIdx.x & 63) < static_cast<unsigned>(S) && p.ordinal == n);
 }
 
+// Top-k of one token's E logits by one wave, as wave_topk gives it, for a short
+// list: the top_k-th largest of the lanes' maxima is a bound that all of the
+// top_k largest logits reach, few others do, and the reaching ones, one per
+// lane, are ranked by counting.  A token with more than 64 of them (ties) goes
+// to wave_topk.  2 us less than its top_k dependent rounds at top_k = 10.
+template <int NPL>
+__device__ __forceinline__ void small_topk(const float* __restrict__ row, int E, int top_k,
+                                           uint64_t* list, int& my_id, float& my_logit,
+                                           float& top_logit) {
+  const int lane = threadIdx.x & 63;
+  uint64_t key[NPL], best = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = lane + 64 * i;
+    key[i] = e < E ? logit_key(row[e], e) : 0ull;
+    best = max64(best, key[i]);
+  }
+  // the rank of this lane's maximum among the lanes' (keys are distinct; lanes
+  // without an expert hold 0 and tie, behind all others)
+  const uint32_t hi = static_cast<uint32_t>(best >> 32), lo = static_cast<uint32_t>(best);
+  int rank = 0;
+#pragma unroll
+  for (int q = 0; q < 64; ++q) {
+    const uint64_t other = (static_cast<uint64_t>(__builtin_amdgcn_readlane(hi, q)) << 32) |
+                           static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, q));
+    rank += other > best;
+  }
+  const unsigned long long bound_lane = __ballot(rank == min(top_k, min(E, 64)) - 1);
+  uint64_t bound = 0;
+  if (top_k <= 64 && bound_lane) {
+    const int q = __builtin_ctzll(bound_lane);
+    bound = (static_cast<uint64_t>(__builtin_amdgcn_readlane(hi, q)) << 32) |
+            static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, q));
+  }
+  int found = 0;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const bool in = key[i] != 0 && key[i] >= bound;
+    const unsigned long long who = __ballot(in);
+    const int at = found + __popcll(who & ((1ull << lane) - 1ull));
+    if (in && at < 64) list[at] = key[i];
+    found += __popcll(who);
+  }
+  if (found > 64) return wave_topk<NPL>(row, E, top_k, my_id, my_logit, top_logit);
+  const uint64_t mine = lane < found ? list[lane] : 0;
+  int place = 0;
+  for (int q = 0; q < found; ++q) place += list[q] > mine;
+  // sorted, then each lane takes its rank's
+  if (lane < found) list[place] = mine;
+  const uint64_t k = lane < found ? list[lane] : 0;
+  my_id = lane < top_k ? key_expert(k) : -1;
+  my_logit = lane < top_k ? key_logit(k) : 0.f;
+  top_logit = key_logit(list[0]);
+}
+
 // One window of 512 values of a weight row and of a token's row, as in the
 // streaming product: lane group g takes block 4 i + g at step i.
 struct WeightWindow {
@@ -68,7 +123,13 @@ __device__ __forceinline__ void load_window(WeightWindow& b, const Weights& w, i
   for (int i = 0; i < 4; ++i) {
     const int blk = b0 + 4 * i + g;
     b.w[i] = buffer_load16(w.codes, blk < w.blocks ? w.at + blk * 16 : kOutOfRange);
-    b.s[i] = buffer_load4(w.scales, b0 + 4 * i < w.blocks ? w.scales_at + b0 + 4 * i : kOutOfRange);
+  }
+  if (b0 + 12 < w.blocks) {
+    b.s = buffer_load16(w.scales, w.scales_at + b0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      b.s[i] = buffer_load4(w.scales, b0 + 4 * i < w.blocks ? w.scales_at + b0 + 4 * i : kOutOfRange);
   }
 }
 
@@ -91,13 +152,14 @@ __device__ __forceinline__ void multiply_window(f32x4& acc, const WeightWindow& 
   }
 }
 
-constexpr int kInFlight = 4;  // windows
+constexpr int kInFlight = 2;  // windows
 
 // ---- gate/up -------------------------------------------------------------------
 template <int NPL, typename TX>
 __global__ __launch_bounds__(256) void small_gate_up_kernel(MxSmallArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int ids[kMaxSlots];
+  __shared__ uint64_t lists[kMaxTokens][64];
   __shared__ float h[4][16][17];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -111,7 +173,8 @@ __global__ __launch_bounds__(256) void small_gate_up_kernel(MxSmallArgs p) {
   if (wave < p.T) {
     int id;
     float logit, top;
-    wave_topk<NPL>(p.logits + static_cast<size_t>(wave) * p.E, p.E, p.top_k, id, logit, top);
+    small_topk<NPL>(p.logits + static_cast<size_t>(wave) * p.E, p.E, p.top_k, lists[wave], id,
+                    logit, top);
     const float w = wave_topk_weight(logit, top, p.top_k);
     if (lane < p.top_k) {
       const int s = wave * p.top_k + lane;
