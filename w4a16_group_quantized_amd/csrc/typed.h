@@ -37,8 +37,10 @@ struct __attribute__((packed, aligned(2), may_alias)) Unaligned16 { dwords4 d; }
 __device__ __forceinline__ dwords4 load16(const void* p) {
   return reinterpret_cast<const Unaligned16*>(p)->d;
 }
+// Nontemporal: what these operators write is far larger than the caches (rows
+// moved at 4096 tokens x 10: 41 -> 38 us).
 __device__ __forceinline__ void store16(void* p, dwords4 d) {
-  reinterpret_cast<Unaligned16*>(p)->d = d;
+  __builtin_nontemporal_store(d, &reinterpret_cast<Unaligned16*>(p)->d);
 }
 
 template <typename T>
