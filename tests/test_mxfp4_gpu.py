@@ -164,6 +164,7 @@ PRODUCTS = [  # E, rows, N, K
     (3, 40, 96, 640), (8, 80, 80, 2560), (8, 1000, 130, 96), (37, 90, 48, 544), (512, 80, 64, 256),
     (64, 2500, 160, 256), (4096, 60, 32, 64), (2, 700, 320, 1024),
     (1, 1100, 300, 1440), (3, 2000, 520, 256), (16, 300, 260, 800), (16, 700, 136, 96),
+    (1000, 12000, 64, 160), (600, 20000, 256, 96), (4096, 40000, 32, 64),
 ]
 
 
@@ -226,6 +227,32 @@ def test_product_of_mapped_rows(ops):
                                      row_slots=_gpu(slots), top_k=k)
     _close(got, want, size, K)
     assert (got[4] == 0).all() and (got[40] == 0).all()
+
+
+def test_product_past_32_bits(ops):
+    """More than 2^32 bytes of output, and more than 2^31 of A's codes: rows near both ends."""
+    rng = np.random.default_rng(6)
+    R, N, K = 70000, 32768, 64
+    a, w = _random_mx(rng, R, K), _random_mx(rng, 1, N, K)
+    got = ops.moe_mxfp4_grouped_gemm(_gpu(a[0]), _gpu(a[1]), _gpu(w[0]), _gpu(w[1]), dtype=torch.bfloat16)
+    assert got.numel() * 2 > 1 << 32
+    for rows in (slice(0, 3), slice(65534, 65538), slice(R - 3, R)):
+        want, size = ref.mx_product(ref.mx_values(a[0][rows], a[1][rows]), ref.mx_values(*w), [0, rows.stop - rows.start])
+        _close(got[rows], want, size, K)
+    del got
+    R, N, K = 140000, 32, 32768
+    a_codes = torch.randint(-(1 << 31), 1 << 31, (R, K // 8), device="cuda", dtype=torch.int32)
+    a_scales = torch.full((R, ref.mx_scale_bytes(K)), 126, device="cuda", dtype=torch.uint8)
+    w = _random_mx(rng, 1, N, K)
+    assert a_codes.numel() * 4 > 1 << 31
+    got = ops.moe_mxfp4_grouped_gemm(a_codes, a_scales, _gpu(w[0]), _gpu(w[1]))
+    slots = torch.arange(R, dtype=torch.int32, device="cuda")
+    mapped = ops.moe_mxfp4_grouped_gemm(a_codes, a_scales, _gpu(w[0]), _gpu(w[1]), row_slots=slots)
+    for rows in (slice(0, 3), slice(131070, 131075), slice(R - 3, R)):
+        want, size = ref.mx_product(ref.mx_values(_host(a_codes[rows]), _host(a_scales[rows])), ref.mx_values(*w),
+                                    [0, rows.stop - rows.start])
+        _close(got[rows], want, size, K)
+        _close(mapped[rows], want, size, K)
 
 
 @pytest.mark.parametrize("R", [9, 700])
@@ -310,6 +337,21 @@ def test_gate_up_of_mapped_rows_leaves_other_rows_alone(ops):
     n = int(off[-1])
     _check_act(codes[:n], scales[:n], h[:n], size[:n], I, K)
     assert (codes[n:] == -5).all() and (scales[n:] == 99).all()
+
+
+@pytest.mark.parametrize("R", [4, 40, 300])
+def test_gate_up_of_a_nan_row_is_a_nan_row(ops, R):
+    """A NaN scale in a token's row: scale byte 255 and zero codes in all its blocks, the other
+    rows as without it."""
+    rng = np.random.default_rng(R)
+    I, K = 96, 256
+    a, w = _random_mx(rng, R, K, low=124, high=126), _random_mx(rng, 1, 2 * I, K, low=120, high=122)
+    clean = ops.moe_mxfp4_gate_up(_gpu(a[0]), _gpu(a[1]), _gpu(w[0]), _gpu(w[1]))
+    a[1][2, 3] = 255
+    codes, scales = ops.moe_mxfp4_gate_up(_gpu(a[0]), _gpu(a[1]), _gpu(w[0]), _gpu(w[1]))
+    assert (codes[2] == 0).all() and (scales[2, : I // 32] == 255).all()
+    keep = [r for r in range(R) if r != 2]
+    assert torch.equal(codes[keep], clean[0][keep]) and torch.equal(scales[keep], clean[1][keep])
 
 
 # ---- the layer --------------------------------------------------------------------
