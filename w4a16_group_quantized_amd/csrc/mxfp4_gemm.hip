@@ -539,7 +539,11 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
       cut(st, blocks - S::CB * c);
       wait_lds_and_barrier();
     }
+    // a wave that multiplies goes before one that asks for loads (the dense
+    // product of 8191 x 8192 x 8192: 290 -> 285 us)
+    if constexpr (S::NW * S::NT >= 8) __builtin_amdgcn_s_setprio(1);
     compute(st);
+    if constexpr (S::NW * S::NT >= 8) __builtin_amdgcn_s_setprio(0);
     stage = stage + S::kStage == S::STAGES * S::kStage ? 0 : stage + S::kStage;
     if (++c == chunks) {
       c = 0;
