@@ -259,7 +259,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
   // ---- loads: the tile and chunk that are requested next
   Descriptor rw, rws, ra, ras;
   uint32_t at_w[S::kLoadW], at_t[S::kLoadT], at_ws[S::kScaleW], at_ts[S::kScaleT];
-  auto swizzle = [](int row) { return row & 7; };
+  auto swizzle = [](int row) { return (row >> 1) & 7; };
   // the set of rows whose scales this wave loads; spare waves repeat a load
   auto scale_set = [&](int i, int sets) { return (i * S::kWaves + wave) % sets; };
   auto aim = [&](const Tile& t) {
@@ -363,7 +363,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
     struct Step {
       dwords4 w[S::NW], t[S::NT];
     };
-    struct Scales {
+    struct alignas(S::CB) Scales {
       uint32_t v[S::CB / 4];
     };
     auto read = [&](int s) {
@@ -431,9 +431,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
       if constexpr (!GATE_UP) {
         const bool none = row < tl.r1 && p.row_slots != nullptr && a_row(p, row) < 0;
         constexpr int kCols = S::kTurn / kBytes<TO>, kSlots = S::kTurn / 16, kRows = 64 / kSlots;
-        auto slot = [](int t, int n) {
-          return (n ^ (kSlots == 8 ? t : t >> 1)) & (kSlots - 1);
-        };
+        auto slot = [](int t, int n) { return (n ^ t) & (kSlots - 1); };
 #pragma unroll
         for (int c0 = 0; c0 < S::NW * 32; c0 += kCols) {
 #pragma unroll
