@@ -615,8 +615,9 @@ size_t moe_mxfp4_layer_workspace_bytes(int64_t T, int32_t top_k, int32_t E,
  * moe_mxfp4_layer_forward - moe_layer_forward on MXFP4 experts, activations
  * quantised too: moe_route_permute, moe_mxfp4_quantize of x, moe_mxfp4_gate_up
  * over moe_permute's sorted_slots, moe_mxfp4_grouped_gemm into fp32 rows and
- * moe_combine_masked, in one call; out is what those calls produce, bit for
- * bit.
+ * moe_combine_masked, in one call; out is what those calls produce up to the
+ * order of the products' fp32 sums (up to 4 tokens two launches do all of it;
+ * from 5 tokens on the kernels are the calls' own).
  *
  *   logits      in   fp32 [T, E]
  *   x, out      in, out  dtype [T, H], dense

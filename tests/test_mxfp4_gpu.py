@@ -399,6 +399,27 @@ def test_layer_is_its_calls_and_near_the_oracle(ops, T, E, k, H, I, dtype):
     assert np.sqrt((off ** 2).sum() / (want ** 2).sum()) <= 1e-2
 
 
+def test_a_model_s_weights_through_the_layer(ops):
+    """Float weights quantised at load time, expert by expert rows at once, then a decode and a
+    prefill call on them."""
+    rng = np.random.default_rng(17)
+    E, k, H, I = 6, 2, 192, 96
+    w13 = torch.from_numpy(rng.standard_normal((E, 2 * I, H)).astype(np.float32)).cuda() / H ** 0.5
+    w2 = torch.from_numpy(rng.standard_normal((E, H, I)).astype(np.float32)).cuda() / I ** 0.5
+    w, values = {}, {}
+    for name, t in (("w13", w13), ("w2", w2)):
+        codes, scales = ops.moe_mxfp4_quantize(t.flatten(0, 1))
+        w[name + "_codes"], w[name + "_scales"] = (a.view(*t.shape[:2], -1) for a in (codes, scales))
+        values[name] = ref.mx_values(_host(w[name + "_codes"]), _host(w[name + "_scales"]))
+        assert np.array_equal(values[name], ref.mx_values(*ref.mx_pack(*ref.mx_quantize(_host(t.flatten(0, 1))))).reshape(t.shape))
+    for T in (1, 30):
+        logits = torch.randn(T, E, device="cuda")
+        x = torch.randn(T, H, device="cuda", dtype=torch.float16)
+        out = ops.moe_mxfp4_layer_forward(logits, x, k, w)
+        want = ref.mx_layer(logits.cpu().numpy(), _host(x), k, values["w13"], values["w2"])
+        assert np.sqrt(((_host(out) - want) ** 2).sum() / (want ** 2).sum()) <= 1e-2
+
+
 @pytest.mark.parametrize("T,E,k", [(1, 512, 10), (3, 100, 7), (4, 37, 16), (1, 1000, 60), (9, 64, 5)])
 def test_layer_with_tied_logits(ops, T, E, k):
     """Few distinct logits, all equal ones, and a list of choices longer than a wave's lanes hold:

@@ -10,7 +10,10 @@
 //
 // All are bound by memory.  Rows move in 16-byte accesses at any alignment;
 // sums are fp32 in a fixed order, so a repeated call gives identical bits.
-// Rows that no slot points at are neither read nor written.
+// Rows that no slot points at are neither read nor written.  4096 tokens x 10 x
+// 2560 bf16, a tenth of the tokens without experts: dispatch 38 us (5.5 TB/s),
+// combine 43 (4.9), combine backward 82 (4.9); 1021 tokens in fp32, dispatch
+// backward 18.6 us (5.6).
 #include "mxfp4.h"
 #include "typed.h"
 

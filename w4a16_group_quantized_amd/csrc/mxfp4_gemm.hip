@@ -20,12 +20,15 @@ namespace moe {
 namespace {
 
 // ---------------------------------------------------------------- streaming --
-// Few rows per expert: bound by reading each active expert's weights once.
-// A wave takes 16 weight rows over all of K, straight from memory to
-// registers in windows of 512 values (a row's 256 bytes of codes and 16 bytes
+// Few rows of few experts: bound by the latency of reading each active expert's
+// weights once.  A wave takes 16 weight rows over all of K, straight from memory
+// to registers in windows of 512 values (a row's 256 bytes of codes and 16 bytes
 // of scales), two windows in flight; the up to 16 tokens of its tile come
 // through the caches.  Four waves make a workgroup: 64 output columns, or the
-// two halves of gate and up of 32 columns of I.
+// two halves of gate and up of 32 columns of I.  10 rows of 512 experts,
+// 1280 x 2560: 9.6 us for 17 MB (11.8 with the tiles below, whose hundred
+// workgroups leave half of the compute units idle); three windows in flight or
+// five waves per SIMD are slower.
 constexpr int kTokens = 16;
 
 struct Window {
@@ -135,6 +138,12 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxGemmArgs p, int n_tile
 // multiplied and stored.  In LDS a row's blocks are stored with their number
 // xor a few bits of the row's, so that the 16-byte reads of 8 neighbouring rows
 // meet different banks.
+//
+// 512 experts, 1280 x 2560: 217 us for 40960 rows (4.85 TB/s, bound by memory;
+// one workgroup per tile, without the running ring, 252), 29 us for 80 rows
+// (4.4 TB/s).  One expert, 8191 x 8192 x 8192: 285 to 300 us, 3.7 to 3.9
+// PFLOP/s, half of the cycles in matrix instructions at the clock it runs at;
+// bound by the loads of a chunk and its products overlapping in two stages only.
 //
 // Tokens behind a segment and weight rows behind N leave what LDS holds, or
 // rows that follow: each result depends on its own row and token only, and
@@ -552,7 +561,10 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
   __builtin_amdgcn_s_waitcnt(0x0F70);
 }
 
-// Shapes, named by their tokens; 32 tokens in a deep ring and in a short one.
+// Shapes, named by their tokens.  Those of 32 tokens take several workgroups per
+// compute unit, two with a deep ring (K > 1024: 2560 rows of 512 experts, gate/up,
+// 160 us against 164) or three with a short one (K = 640: 80 rows 19.4 against
+// 22.9, 640 rows 80 against 88); the larger shapes fill LDS.
 using Tile32 = TileShape<128, 32, 2, 1, 3>;
 using Tile32Short = TileShape<128, 32, 2, 1, 2>;
 using Tile64 = TileShape<256, 64, 4, 2, 3>;
@@ -603,9 +615,12 @@ void launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
   // the tile kernels address mapped rows of A with 31-bit offsets
   const bool far = a.row_slots != nullptr && a.a_rows * (a.K / 2) >= (static_cast<int64_t>(1) << 31);
   const int64_t weights = static_cast<int64_t>(active) * a.N * (a.K / 2);
+  // gate/up of 512 experts, stream / tiles: 10 rows (17 MB) 9.6 / 11.8 us, 20 rows
+  // (35 MB) 13.0 / 12.2, 80 rows 34.6 / 32.1, 2560 rows 216 / 160
   if (far || (mean <= 8 && weights <= 32 << 20)) return launch_stream(a, stream);
   // the tile that holds the mean, or a smaller one where its tiles would leave
-  // compute units without any
+  // compute units without any (8192 x 8192 weights: 128 rows 46 us in 32 tiles of
+  // 256 x 128, 21 in 256 of 128 x 32; 512 rows 63 and 39)
   const auto enough = [&](int bw, int bt) {
     return static_cast<int64_t>(active) * ((mean + bt - 1) / bt) * ((a.N + bw - 1) / bw) >=
            device_info().cus;

@@ -9,7 +9,8 @@
 // Both are bound by memory: one pass, 8 values (one code word) per lane, so
 // loads and code stores of a wave are contiguous; the four lanes of a block
 // meet by DPP inside their quad.  m is the largest bit pattern with the sign
-// cleared, so an infinity or a NaN shows in the same maximum.
+// cleared, so an infinity or a NaN shows in the same maximum.  81920 x 2560
+// bf16: 90 us there (5.9 TB/s), 85 us back (6.2 TB/s).
 #include "mxfp4.h"
 #include "mxfp4_tile.h"
 #include "typed.h"

@@ -616,7 +616,8 @@ def weights_to_device(host: dict, device="cuda") -> dict:
 # MXFP4 experts, and token rows to expert order and back
 #
 # These calls check their tensors (device, type, shape, layout) and run on the
-# tensors' own device, on that device's current stream.
+# tensors' own device, on that device's current stream.  Gradients are calls of
+# their own: nothing here records an autograd graph.
 # --------------------------------------------------------------------------- #
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
