@@ -163,6 +163,7 @@ struct TileShape {
   static constexpr int kScaleW = (kSetsW + kWaves - 1) / kWaves;
   static constexpr int kScaleT = (kSetsT + kWaves - 1) / kWaves;
   static constexpr int kLoads = kLoadW + kLoadT + kScaleW + kScaleT;  // per wave and chunk
+  static constexpr bool kTrim = BT == 32 && STAGES == 2;      // leave out blocks behind K
   static constexpr int kTurn = 128, kScratch = 32 * kTurn;    // results turn per wave, below
   static constexpr int kLds = STAGES * kStage + static_cast<int>(sizeof(TileTable));
   static constexpr int kPerCu = static_cast<int>(kGfx950LdsBytes) / kLds;
@@ -320,14 +321,26 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
   // Requests the next chunk.  Behind the last one the loads go to empty ranges
   // (nothing is fetched), so that the number on their way is always the same.
   auto load_next = [&]() {
+    // Blocks of a last chunk that lie behind K belong to the next row.  The shape
+    // for short K does not read them: at K = 640 they are a fifth of the weights'
+    // bytes again (2560 rows of 512 experts 106 -> 104 us, 10240 rows 120 -> 117);
+    // the test for it costs the others 1%.
+    const int live = blocks - S::CB * load_chunk;
+    auto behind = [&](int i) -> uint32_t {
+      const int row = (i * S::kWaves + wave) * S::kRowsPerLoad + lane / S::CB;
+      return (lane % S::CB ^ swizzle(row)) >= live ? kOutOfRange : 0u;
+    };
+    const bool whole = !S::kTrim || live >= S::CB;
 #pragma unroll
     for (int i = 0; i < S::kLoadW; ++i) {
-      load16_to_lds(rw, load_at + (i * S::kWaves + wave) * 1024, at_w[i]);
+      load16_to_lds(rw, load_at + (i * S::kWaves + wave) * 1024,
+                    whole ? at_w[i] : at_w[i] | behind(i));
       at_w[i] += S::kRow;
     }
 #pragma unroll
     for (int i = 0; i < S::kLoadT; ++i) {
-      load16_to_lds(ra, load_at + S::BW * S::kRow + (i * S::kWaves + wave) * 1024, at_t[i]);
+      load16_to_lds(ra, load_at + S::BW * S::kRow + (i * S::kWaves + wave) * 1024,
+                    whole ? at_t[i] : at_t[i] | behind(i));
       at_t[i] += S::kRow;
     }
 #pragma unroll
@@ -344,9 +357,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, i
     load_at = load_at == ring_at + (S::STAGES - 1) * S::kStage ? ring_at : load_at + S::kStage;
     ++load_chunk;
   };
-  // Aims at the next tile when all of this one's chunks are requested.  Called
-  // apart from load_next, which so has no branches and stays one block with the
-  // products around it.
+  // Aims at the next tile when all of this one's chunks are requested.
   auto aim_next = [&]() {
     if (load_chunk < chunks) return;
     load_chunk = 0;
