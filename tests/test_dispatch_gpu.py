@@ -159,6 +159,36 @@ def test_combine_and_its_gradients(ops, T, k, E, H, y_dtype):
         _close(gw, want_w, size_w, H)
 
 
+@pytest.mark.parametrize("seed", range(16))
+def test_random_moves(ops, seed):
+    """Any sizes and kinds of ids through permutation, dispatch, combine and their gradients."""
+    rng = np.random.default_rng(seed)
+    T = int(np.exp(rng.uniform(0, np.log(1500))))
+    k, E = int(rng.integers(1, 13)), int(rng.choice([1, 3, 50, 513, 4096]))
+    H = int(np.exp(rng.uniform(0, np.log(400))))
+    first = int(rng.integers(0, 3))
+    ids = _ids(rng, T, k, E, ["all", "some", "one", "wild"][seed % 4])
+    y_dtype, dtype = DTYPES[seed % 3], DTYPES[(seed // 3) % 3]
+    print(T, k, E, H, first, y_dtype, dtype, flush=True)
+    perm = ops.moe_permute_masked(torch.from_numpy(ids).cuda(), E, first_expert=first)
+    want = ref.permute_masked(ids, E, first)
+    _check_perm(perm, want)
+    rows, R = perm["slot_rows"], T * k
+    x = torch.randn(T, H, device="cuda").to(y_dtype)
+    out = ops.moe_dispatch(x, rows, k)
+    assert np.array_equal(_host(out), ref.dispatch(_host(x), want["slot_rows"], k, np.zeros((R, H), np.float32)))
+    w = torch.randn(T, k, device="cuda")
+    got = ops.moe_combine_masked(out, w, rows, dtype=dtype)
+    value, size = ref.combine_masked(_host(out), _host(w), want["slot_rows"])
+    _close(got, value, size, k)
+    gy, gw = ops.moe_combine_backward(got, out, w, rows)
+    value_y, value_w, size_w = ref.combine_backward(_host(got), _host(out), _host(w), want["slot_rows"], np.zeros((R, H)))
+    _close(gy, value_y, np.abs(value_y), 1)
+    _close(gw, value_w, size_w, H)
+    value, size = ref.combine_masked(_host(gy), np.ones((T, k)), want["slot_rows"])
+    _close(ops.moe_dispatch_backward(gy, rows, k), value, size, k)
+
+
 def test_combine_gradients_against_differences(ops):
     """The outputs are linear in the rows and in the weights, so a difference of the fp64 oracle
     over a step of 1 is the directional derivative."""

@@ -211,6 +211,35 @@ def test_product_leaves_other_rows_and_columns_alone(ops, R, E):
         assert (buf == 7.0).all()
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_random_products(ops, seed):
+    """Any sizes: dense and grouped, rows in order and mapped, strided outputs, gate/up."""
+    rng = np.random.default_rng(1000 + seed)
+    E = int(rng.choice([1, 2, 7, 64, 300, 700]))
+    R = int(np.exp(rng.uniform(0, np.log(3000))))
+    K = 32 * int(np.exp(rng.uniform(0, np.log(60))))
+    N = int(np.exp(rng.uniform(0, np.log(900))))
+    mapped = bool(rng.integers(2))
+    k = int(rng.integers(1, 5)) if mapped else 1
+    T = -(-R // k)
+    a, w = _random_mx(rng, T if mapped else R, K), _random_mx(rng, E, N, K, low=118, high=124)
+    slots = rng.integers(0, T * k, size=R).astype(np.int32)
+    off = _offsets(rng, E, R)
+    want, size = ref.mx_product(ref.mx_values(*a), ref.mx_values(*w), off, slots // k if mapped else None)
+    dtype = DTYPES[seed % 3]
+    buf = torch.full((R, N + 3), 7.0, device="cuda", dtype=dtype)
+    args = [_gpu(t) for t in (*a, *w, off)]
+    more = {"row_slots": _gpu(slots), "top_k": k} if mapped else {}
+    print(E, R, N, K, mapped, k, dtype, flush=True)
+    out = ops.moe_mxfp4_grouped_gemm(*args, **more, out=buf[:, 2:2 + N])
+    _close(out, want, size, K)
+    assert (buf[:, :2] == 7).all() and (buf[:, 2 + N:] == 7).all()
+    I = 32 * max(1, N // 64)
+    w = _random_mx(rng, E, 2 * I, K, low=116, high=120)
+    h, size = ref.mx_product(ref.mx_values(*a), ref.mx_values(*w), off, slots // k if mapped else None)
+    _check_act(*ops.moe_mxfp4_gate_up(args[0], args[1], _gpu(w[0]), _gpu(w[1]), args[4], **more), h, size, I, K)
+
+
 def test_product_of_mapped_rows(ops):
     """row_slots: rows of tokens through the slots that hold them; a slot outside the tokens is a
     row of zeros."""

@@ -288,7 +288,7 @@ static MxLayerWs mx_layer_ws(void* base, int64_t T, int32_t top_k, int32_t E, in
   w.slot_rows = reinterpret_cast<int32_t*>(take(4 * S));
   w.active = reinterpret_cast<int32_t*>(take(4 * static_cast<size_t>(E)));
   w.num_active = reinterpret_cast<int32_t*>(take(4));
-  w.perm_bytes = permute_workspace_bytes(T, E);
+  w.perm_bytes = permute_masked_workspace_bytes(T, top_k, E);
   w.perm = take(w.perm_bytes);
   w.x_codes = reinterpret_cast<int32_t*>(take(S * (H / 2)));
   w.x_scales = reinterpret_cast<uint8_t*>(take(S * mx_scale_bytes(H)));
@@ -349,9 +349,18 @@ int moe_mxfp4_layer_forward(const float* logits, const void* x, int32_t dtype, i
     launch_mx_small_layer(a, static_cast<hipStream_t>(stream));
     return check_launch();
   }
-  if (int st = moe_route_permute(logits, T, E, top_k, w.ids, w.weights, w.offsets, w.sorted,
-                                 w.slot_rows, w.active, w.num_active, w.perm, w.perm_bytes, stream))
-    return st;
+  // one launch for few tokens; otherwise the masked permutation, which drops
+  // nothing here: moe_permute's result in one launch less
+  if (T <= kPermBlockTokens) {
+    if (int st = moe_route_permute(logits, T, E, top_k, w.ids, w.weights, w.offsets, w.sorted,
+                                   w.slot_rows, w.active, w.num_active, nullptr, 0, stream))
+      return st;
+  } else {
+    if (int st = moe_route(logits, T, E, top_k, w.ids, w.weights, stream)) return st;
+    if (int st = moe_permute_masked(w.ids, T, top_k, 0, E, w.offsets, w.sorted, w.slot_rows,
+                                    w.active, w.num_active, w.perm, w.perm_bytes, stream))
+      return st;
+  }
   // every token once, stored to its rows: the products then read rows in order
   launch_mx_quantize(x, dtype, T, H, H, w.x_codes, w.x_scales, w.slot_rows, top_k,
                      static_cast<int>(S), static_cast<hipStream_t>(stream));
