@@ -627,17 +627,11 @@ _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 def _device_of(*tensors) -> int:
     """Index of the one GPU that all the given tensors (None: absent) are on."""
-    dev = -1
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0:
-                raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, not on a GPU")
-            if d != dev:
-                if dev >= 0:
-                    raise ValueError(f"a tensor of shape {tuple(t.shape)} is on GPU {d}, the ones "
-                                     f"before it on GPU {dev}")
-                dev = d
+        if t is not None and (t.get_device() != dev or dev < 0):
+            where = "not on a GPU" if t.get_device() < 0 else f"others are on {tensors[0].device}"
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, {where}")
     return dev
 
 
@@ -682,10 +676,9 @@ def _matrix(name: str, t: torch.Tensor):
     code = _DTYPE.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} is {t.dtype}, not float32, float16 or bfloat16")
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} has shape {tuple(shape)}, not two dimensions")
-    rows, cols = shape
+    if t.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not two dimensions")
+    rows, cols = t.shape
     if t.is_contiguous():
         return t.data_ptr(), code, cols, rows, cols
     if cols > 1 and t.stride(1) != 1:
@@ -704,6 +697,15 @@ def _sized(name: str, t: torch.Tensor, rows: int, cols: int, code: int | None = 
     if code is not None and got != code:
         raise ValueError(f"{name} is {t.dtype}, not the type of the tensor that it goes with")
     return ptr, got, stride
+
+
+def _made(like: torch.Tensor, rows: int, cols: int, dtype: torch.dtype):
+    """(matrix, pointer, dtype code, row stride) of an output made here."""
+    code = _DTYPE.get(dtype)
+    if code is None:
+        raise ValueError(f"dtype {dtype} is not float32, float16 or bfloat16")
+    out = like.new_empty((rows, cols), dtype=dtype)
+    return out, out.data_ptr(), code, cols
 
 
 def _apart(name: str, out: torch.Tensor, **inputs) -> None:
@@ -741,6 +743,19 @@ def mxfp4_scale_bytes(K: int) -> int:
 
 def _mx(name: str, codes: torch.Tensor, scales: torch.Tensor, dims: int):
     """(codes pointer, scales pointer, shape with K in place of its words) of an MXFP4 tensor."""
+    if codes.dim() == dims:  # the usual case, at the least cost
+        if dims == 2:
+            rows, words = codes.shape
+            want = (rows, (words + 15) // 16 * 4)
+            shape = (rows, words * 8)
+        else:
+            experts, rows, words = codes.shape
+            want = (experts, rows, (words + 15) // 16 * 4)
+            shape = (experts, rows, words * 8)
+        if (codes.dtype is torch.int32 and scales.dtype is torch.uint8 and scales.shape == want
+                and not words % 4 and 0 < words <= 8192 and codes.is_contiguous()
+                and scales.is_contiguous()):
+            return codes.data_ptr(), scales.data_ptr(), shape
     shape = codes.shape
     if len(shape) != dims:
         raise ValueError(f"{name} codes have shape {tuple(shape)}, not {dims} dimensions")
@@ -775,8 +790,9 @@ def moe_mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor,
     """The values of MXFP4 rows, rounded to dtype (or out's type): [R, K]."""
     pc, ps, (R, K) = _mx("x", codes, scales, 2)
     if out is None:
-        out = codes.new_empty((R, K), dtype=dtype)
-    ptr, code, stride = _sized("out", out, R, K)
+        out, ptr, code, stride = _made(codes, R, K, dtype)
+    else:
+        ptr, code, stride = _sized("out", out, R, K)
     _run("moe_mxfp4_dequantize", _device_of(codes, scales, out), pc, ps, R, K, ptr, code, stride)
     return out
 
@@ -805,8 +821,9 @@ def moe_mxfp4_grouped_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_code
     args, rows, N, K = _product_args(a_codes, a_scales, w_codes, w_scales, expert_offsets,
                                      row_slots, top_k)
     if out is None:
-        out = a_codes.new_empty((rows, N), dtype=dtype)
-    ptr, code, stride = _sized("out", out, rows, N)
+        out, ptr, code, stride = _made(a_codes, rows, N, dtype)
+    else:
+        ptr, code, stride = _sized("out", out, rows, N)
     _run("moe_mxfp4_grouped_gemm",
          _device_of(a_codes, a_scales, w_codes, w_scales, expert_offsets, row_slots, out), *args, N,
          K, ptr, code, stride)
@@ -905,7 +922,9 @@ def _weights(topk_weights: torch.Tensor):
     if topk_weights.dim() != 2:
         raise ValueError(f"topk_weights has shape {tuple(topk_weights.shape)}, not [T, top_k]")
     T, k = topk_weights.shape
-    return _dense("topk_weights", topk_weights, torch.float32, T, k), T, k
+    if topk_weights.dtype is not torch.float32 or not topk_weights.is_contiguous():
+        raise ValueError(f"topk_weights must be contiguous float32, is {topk_weights.dtype}")
+    return topk_weights.data_ptr(), T, k
 
 
 def moe_dispatch(x: torch.Tensor, slot_rows: torch.Tensor, top_k: int,
@@ -933,8 +952,10 @@ def moe_dispatch_backward(grad_sorted: torch.Tensor, slot_rows: torch.Tensor, to
     pg, dtype, sg, rows, H = _matrix("grad_sorted", grad_sorted)
     if out is None:
         out = grad_sorted.new_empty((T, H))
-    po, _, so = _sized("out", out, T, H, dtype)
-    _apart("out", out, grad_sorted=grad_sorted)
+        po, so = out.data_ptr(), H
+    else:
+        po, _, so = _sized("out", out, T, H, dtype)
+        _apart("out", out, grad_sorted=grad_sorted)
     _run("moe_dispatch_backward", _device_of(grad_sorted, slot_rows, out), pg, dtype, T, top_k, H,
          sg, pr, rows, po, so)
     return out
@@ -947,9 +968,10 @@ def moe_combine_masked(y_sorted: torch.Tensor, topk_weights: torch.Tensor, slot_
     pw, T, k = _weights(topk_weights)
     py, y_code, sy, rows, H = _matrix("y_sorted", y_sorted)
     if out is None:
-        out = y_sorted.new_empty((T, H), dtype=dtype)
-    po, o_code, so = _sized("out", out, T, H)
-    _apart("out", out, y_sorted=y_sorted)
+        out, po, o_code, so = _made(y_sorted, T, H, dtype or y_sorted.dtype)
+    else:
+        po, o_code, so = _sized("out", out, T, H)
+        _apart("out", out, y_sorted=y_sorted)
     _run("moe_combine_masked", _device_of(y_sorted, topk_weights, slot_rows, out), py, y_code, T, k,
          H, sy, pw, _dense("slot_rows", slot_rows, torch.int32, T * k), rows, po, o_code, so)
     return out
