@@ -184,6 +184,27 @@ def test_grouped_gemm(ops, E, R, N, K):
     assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("E,R,N,K", [
+    (1, 1, 1, 1568), (1, 37, 45, 2048), (5, 60, 200, 4000), (1, 16, 48, 16384), (1, 300, 130, 1600), (9, 50, 77, 1536),
+    (200, 2000, 250, 2080), (500, 9000, 130, 96), (300, 9000, 200, 2080), (40, 4000, 900, 640),
+    (70, 4900, 1000, 352), (3, 6000, 2100, 224), (1, 4001, 4200, 160), (2, 4300, 4100, 288),
+])
+def test_products_of_every_variant(ops, E, R, N, K):
+    """Few columns over a K shared out to waves, then each of the tiles' shapes with odd ends; rows
+    in order and mapped, bit for bit alike twice."""
+    rng = np.random.default_rng(N)
+    a, w = _random_mx(rng, R, K), _random_mx(rng, E, N, K)
+    off = _offsets(rng, E, R, empty=0.0 if R < 100 else 0.2)
+    values = ref.mx_values(*a), ref.mx_values(*w)
+    args = (_gpu(a[0]), _gpu(a[1]), _gpu(w[0]), _gpu(w[1]), _gpu(off))
+    slots = rng.permutation(R).astype(np.int32)
+    for rows, more in ((None, {}), (slots, {"row_slots": _gpu(slots)})):
+        want, size = ref.mx_product(*values, off, rows)
+        got = ops.moe_mxfp4_grouped_gemm(*args, **more)
+        _close(got, want, size, K)
+        assert torch.equal(got, ops.moe_mxfp4_grouped_gemm(*args, **more))
+
+
 @pytest.mark.parametrize("R,N,K", [(1, 40, 96), (33, 128, 256), (515, 384, 544)])
 def test_dense_product_without_offsets(ops, R, N, K):
     rng = np.random.default_rng(R)
@@ -349,6 +370,16 @@ def test_gate_up(ops, E, R, I, K):
     codes, scales = ops.moe_mxfp4_gate_up(_gpu(a[0]), _gpu(a[1]), _gpu(w[0]), _gpu(w[1]), _gpu(off),
                                           out=out)
     _check_act(codes, scales, h, size, I, K)
+
+
+@pytest.mark.parametrize("E,R,I,K", [(1, 5, 64, 1568), (8, 40, 96, 2080), (3, 20, 32, 4096), (2, 1, 160, 8192)])
+def test_gate_up_of_few_rows_with_long_sums(ops, E, R, I, K):
+    rng = np.random.default_rng(K)
+    a = _random_mx(rng, R, K, low=124, high=126)
+    w = _random_mx(rng, E, 2 * I, K, low=120, high=122)
+    off = _offsets(rng, E, R)
+    h, size = ref.mx_product(ref.mx_values(*a), ref.mx_values(*w), off)
+    _check_act(*ops.moe_mxfp4_gate_up(_gpu(a[0]), _gpu(a[1]), _gpu(w[0]), _gpu(w[1]), _gpu(off)), h, size, I, K)
 
 
 def test_gate_up_of_mapped_rows_leaves_other_rows_alone(ops):

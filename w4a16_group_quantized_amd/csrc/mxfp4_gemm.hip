@@ -21,14 +21,20 @@ namespace {
 
 // ---------------------------------------------------------------- streaming --
 // Few rows of few experts: bound by the latency of reading each active expert's
-// weights once.  A wave takes 16 weight rows over all of K, straight from memory
-// to registers in windows of 512 values (a row's 256 bytes of codes and 16 bytes
-// of scales), two windows in flight; the up to 16 tokens of its tile come
-// through the caches.  Four waves make a workgroup: 64 output columns, or the
-// two halves of gate and up of 32 columns of I.  10 rows of 512 experts,
-// 1280 x 2560: 9.6 us for 17 MB (11.8 with the tiles below, whose hundred
-// workgroups leave half of the compute units idle); three windows in flight or
-// five waves per SIMD are slower.
+// weights once.  A wave takes 16 weight rows, straight from memory to registers
+// in windows of 512 values of K (a row's 256 bytes of codes and 16 bytes of
+// scales), two windows in flight; the up to 16 tokens of its tile come through
+// the caches.  Four waves make a workgroup: 64 output columns, or the two halves
+// of gate and up of 32 columns of I.
+//
+// SPLIT > 1 shares the windows of K out, to the four waves of a workgroup that
+// then takes 16 columns, or to twice as many waves of a gate/up workgroup; their
+// sums meet in LDS and are added in the order of the parts.  4096 x 4096, one row:
+// 4.7 us (10.8 unsplit, 8.4 MB); 7168 x 7168, 9.4 us (17.6).  gate/up of 10 rows of
+// 512 experts, 1280 x 2560: 8.8 us for 17 MB (9.6 unsplit, 11.8 with the tiles
+// below, whose hundred workgroups leave half of the compute units idle).  Below
+// four windows the split costs: 20 experts, 2048 x 1280: 8.6 us (7.6 unsplit).
+// Three windows in flight or five waves per SIMD are slower.
 constexpr int kTokens = 16;
 
 struct Window {
@@ -36,8 +42,9 @@ struct Window {
   dwords4 ws, as;
 };
 
-template <bool GATE_UP, typename TO>
-__global__ __launch_bounds__(256) void mx_stream_kernel(MxGemmArgs p, int n_tiles) {
+template <bool GATE_UP, typename TO, int SPLIT>
+__global__ __launch_bounds__(GATE_UP ? 256 * SPLIT : 256) void mx_stream_kernel(MxGemmArgs p,
+                                                                               int n_tiles) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mt = blockIdx.x / n_tiles, nt = blockIdx.x - mt * n_tiles;
@@ -48,8 +55,9 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxGemmArgs p, int n_tile
   const int sbytes = mx_scale_bytes(p.K);
   const int col = lane & 15, g = lane >> 4;
   const int I = p.N / 2;
-  const int n = GATE_UP ? (wave >> 1) * I + nt * 32 + (wave & 1) * 16 + col
-                        : nt * 64 + wave * 16 + col;
+  const int part = GATE_UP ? wave >> 2 : SPLIT > 1 ? wave : 0;  // of K
+  const int n = GATE_UP ? ((wave >> 1) & 1) * I + nt * 32 + (wave & 1) * 16 + col
+                        : (SPLIT > 1 ? nt * 16 : nt * 64 + wave * 16) + col;
   const bool n_ok = n < p.N;
   const auto rw = make_rsrc(p.w_codes + static_cast<int64_t>(e) * p.N * (p.K / 2),
                             static_cast<uint32_t>(p.N) * (p.K / 2));
@@ -107,24 +115,34 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxGemmArgs p, int n_tile
   };
   const int windows = (blocks + 15) / 16;
   Window b0, b1;
-  load(b0, 0);
-  load(b1, 1);
-  for (int w = 0; w < windows; w += 2) {
+  load(b0, part);
+  load(b1, part + SPLIT);
+  for (int w = part; w < windows; w += 2 * SPLIT) {
     compute(b0, w);
-    load(b0, w + 2);
-    if (w + 1 < windows) compute(b1, w + 1);
-    load(b1, w + 3);
+    load(b0, w + 2 * SPLIT);
+    if (w + SPLIT < windows) compute(b1, w + SPLIT);
+    load(b1, w + 3 * SPLIT);
   }
 
   // acc[i] is column n0 + 4 g + i of token r0 + col
-  if constexpr (!GATE_UP) {
+  if constexpr (GATE_UP) {
+    __shared__ float h[4 * SPLIT][16][17];
+    gate_up_epilogue<SPLIT>(acc, h, wave, I, nt, r0, r1 - r0, p.act_codes, p.act_scales);
+  } else if constexpr (SPLIT > 1) {
+    __shared__ float h[4][16][17];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[wave][col][4 * g + i] = acc[i];
+    __syncthreads();
+    const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
+    if (r0 + t >= r1 || nt * 16 + c >= p.N) return;
+    const float sum = ((h[0][t][c] + h[1][t][c]) + h[2][t][c]) + h[3][t][c];
+    static_cast<typename TO::bits*>(p.out)[(r0 + t) * p.out_ld + nt * 16 + c] =
+        from_float(TO{}, sum);
+  } else {
     if (row >= r1) return;
     const int n0 = nt * 64 + wave * 16 + 4 * g;
     auto* o = static_cast<typename TO::bits*>(p.out) + row * p.out_ld + n0;
     store4<TO>(o, p.N - n0, acc);
-  } else {
-    __shared__ float h[4][16][17];
-    gate_up_epilogue(acc, h, wave, I, nt, r0, r1 - r0, p.act_codes, p.act_scales);
   }
 }
 
@@ -602,20 +620,29 @@ void launch_tiles(const MxGemmArgs& a, hipStream_t stream) {
   });
 }
 
+template <bool GATE_UP, int SPLIT>
 void launch_stream(const MxGemmArgs& a, hipStream_t stream) {
-  const bool gate_up = a.act_codes != nullptr;
-  const int n_tiles = gate_up ? a.N / 64 : (a.N + 63) / 64;
+  const int cols = GATE_UP ? 32 : SPLIT > 1 ? 16 : 64;
+  const int n_tiles = ((GATE_UP ? a.N / 2 : a.N) + cols - 1) / cols;
   // an expert's last tile may be partial: at most one more tile per expert
   const int m_tiles = a.rows / kTokens + (a.E < a.rows ? a.E : a.rows);
   const dim3 grid(static_cast<unsigned>(m_tiles) * n_tiles);
-  if (gate_up) {
-    hipLaunchKernelGGL((mx_stream_kernel<true, F32>), grid, dim3(256), 0, stream, a, n_tiles);
-    return;
+  if constexpr (GATE_UP) {
+    hipLaunchKernelGGL((mx_stream_kernel<true, F32, SPLIT>), grid, dim3(256 * SPLIT), 0, stream, a,
+                       n_tiles);
+  } else {
+    with_dtype(a.out_dtype, [&](auto t) {
+      using T = decltype(t);
+      hipLaunchKernelGGL((mx_stream_kernel<false, T, SPLIT>), grid, dim3(256), 0, stream, a, n_tiles);
+    });
   }
-  with_dtype(a.out_dtype, [&](auto t) {
-    using T = decltype(t);
-    hipLaunchKernelGGL((mx_stream_kernel<false, T>), grid, dim3(256), 0, stream, a, n_tiles);
-  });
+}
+
+void launch_stream(const MxGemmArgs& a, bool split, hipStream_t stream) {
+  if (a.act_codes != nullptr)
+    split ? launch_stream<true, 2>(a, stream) : launch_stream<true, 1>(a, stream);
+  else
+    split ? launch_stream<false, 4>(a, stream) : launch_stream<false, 1>(a, stream);
 }
 
 }  // namespace
@@ -626,9 +653,16 @@ void launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
   // the tile kernels address mapped rows of A with 31-bit offsets
   const bool far = a.row_slots != nullptr && a.a_rows * (a.K / 2) >= (static_cast<int64_t>(1) << 31);
   const int64_t weights = static_cast<int64_t>(active) * a.N * (a.K / 2);
-  // gate/up of 512 experts, stream / tiles: 10 rows (17 MB) 9.6 / 11.8 us, 20 rows
+  // gate/up of 512 experts, stream / tiles: 10 rows (17 MB) 8.8 / 11.8 us, 20 rows
   // (35 MB) 13.0 / 12.2, 80 rows 34.6 / 32.1, 2560 rows 216 / 160
-  if (far || (mean <= 8 && weights <= 32 << 20)) return launch_stream(a, stream);
+  const bool light = mean <= 8 && weights <= 32 << 20;
+  // products whose tiles would leave half of the compute units idle, stream /
+  // tiles: 16384 x 16384, one row 30.5 / 48 us; 4096 x 4096, 48 rows 9.9 / 12.7;
+  // 512 x 512 x K 2048 7.2 / 9.1; 32768 x 4096, 16 rows (256 tiles) 23.5 / 15.1
+  const int64_t tiles = static_cast<int64_t>(active) * ((mean + 15) / 16) * ((a.N + 127) / 128);
+  const bool few = a.act_codes == nullptr && tiles <= 128;
+  // the split needs a window for each of four waves
+  if (far || light || few) return launch_stream(a, !far && a.K > 1536, stream);
   // the tile that holds the mean, or a smaller one where its tiles would leave
   // compute units without any (8192 x 8192 weights: 128 rows 46 us in 32 tiles of
   // 256 x 128, 21 in 256 of 128 x 32; 512 rows 63 and 39)

@@ -3,7 +3,7 @@
 // With so few tokens the five launches of the layer's steps (router and
 // permutation, quantisation, gate/up, down, combine) are latency: 33.6 us at one
 // token of 512 experts, 10 chosen, hidden 2560, intermediate 640, for 26 MB of
-// weights; 19.8 us in these two (27 against 44 at two tokens, 51 against 60 at
+// weights; 19.3 us in these two (28 against 44 at two tokens, 49 against 60 at
 // four, 64 against 67 at five, which is left to the others).  Here every
 // workgroup does the small steps for itself:
 //   gate/up  routes the tokens (one wave each) while its other waves quantise
@@ -11,7 +11,7 @@
 //            streaming product does
 //   down     takes 16 columns of H of every active expert, an expert per wave,
 //            meets their rows in LDS and adds them up with the router's weights
-// The sums have the order of the separate steps' streaming kernels.
+// The sums' order is fixed: K's shares of gate/up in turn, down from k = 0 up.
 #include "mxfp4_tile.h"
 #include "route.h"
 
@@ -157,12 +157,16 @@ __device__ __forceinline__ void multiply_window(f32x4& acc, const WeightWindow& 
 constexpr int kInFlight = 2;  // windows; four or six are slower (22.2, 22.6 against 21.1 us)
 
 // ---- gate/up -------------------------------------------------------------------
+// K is shared out to the waves in windows, kParts fours of waves per workgroup: one
+// token 19.3 us (19.9 in one share, 19.8 in four), four tokens 49 (50, 60).
+constexpr int kParts = 2, kWaves = 4 * kParts;
+
 template <int NPL, typename TX>
-__global__ __launch_bounds__(256) void small_gate_up_kernel(MxSmallArgs p) {
+__global__ __launch_bounds__(64 * kWaves) void small_gate_up_kernel(MxSmallArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int ids[kMaxSlots];
   __shared__ uint64_t lists[kMaxTokens][64];
-  __shared__ float h[4][16][17];
+  __shared__ float h[kWaves][16][17];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int S = p.T * p.top_k;
@@ -187,11 +191,11 @@ __global__ __launch_bounds__(256) void small_gate_up_kernel(MxSmallArgs p) {
       }
     }
   }
-  // the waves without a token to route quantise them; all of them when there
-  // is none
-  const int q0 = p.T < 4 ? p.T : 0;
+  // the waves without a token to route quantise them
+  const int q0 = p.T;
+  static_assert(kWaves > kMaxTokens, "some wave quantises");
   if (wave >= q0) {
-    const int words = p.H / 8, total = p.T * words, step = (4 - q0) * 64;
+    const int words = p.H / 8, total = p.T * words, step = (kWaves - q0) * 64;
     for (int i0 = (wave - q0) * 64; i0 < total; i0 += step) {
       const int i = min(i0 + lane, total - 1);  // whole blocks: total is a multiple of 4
       const int t = i / words, c = i - t * words;
@@ -221,7 +225,8 @@ __global__ __launch_bounds__(256) void small_gate_up_kernel(MxSmallArgs p) {
   const int rows = __popcll(mine);
 
   const int col = lane & 15;
-  const int n = (wave >> 1) * p.I + nt * 32 + (wave & 1) * 16 + col;
+  const int n = ((wave >> 1) & 1) * p.I + nt * 32 + (wave & 1) * 16 + col;
+  const int part = wave >> 2;
   const int64_t N = 2 * static_cast<int64_t>(p.I);
   const Weights w{make_rsrc(p.w13_codes + e * N * (p.H / 2), static_cast<uint32_t>(N) * (p.H / 2)),
                   make_rsrc(p.w13_scales + e * N * sbytes, static_cast<uint32_t>(N) * sbytes),
@@ -242,16 +247,17 @@ __global__ __launch_bounds__(256) void small_gate_up_kernel(MxSmallArgs p) {
   const int windows = (blocks + 15) / 16;
   WeightWindow b[kInFlight];
 #pragma unroll
-  for (int i = 0; i < kInFlight; ++i) load_window(b[i], w, i);
+  for (int i = 0; i < kInFlight; ++i) load_window(b[i], w, part + i * kParts);
   f32x4 acc{};
-  for (int win = 0; win < windows; win += kInFlight) {
+  for (int win = part; win < windows; win += kInFlight * kParts) {
 #pragma unroll
     for (int i = 0; i < kInFlight; ++i) {
-      if (win + i < windows) multiply_window(acc, b[i], win + i, blocks, row, word);
-      load_window(b[i], w, win + i + kInFlight);
+      const int at = win + i * kParts;
+      if (at < windows) multiply_window(acc, b[i], at, blocks, row, word);
+      load_window(b[i], w, at + kInFlight * kParts);
     }
   }
-  gate_up_epilogue(acc, h, wave, p.I, nt, r0, rows, p.act_codes, p.act_scales);
+  gate_up_epilogue<kParts>(acc, h, wave, p.I, nt, r0, rows, p.act_codes, p.act_scales);
 }
 
 // ---- down and combine --------------------------------------------------------------
@@ -322,7 +328,7 @@ template <int NPL, typename TX>
 void launch_gate_up(const MxSmallArgs& p, hipStream_t stream) {
   const int S = p.T * p.top_k, active = p.E < S ? p.E : S;
   const size_t lds = static_cast<size_t>(p.T) * (p.H / 2 + mx_scale_bytes(p.H));
-  hipLaunchKernelGGL((small_gate_up_kernel<NPL, TX>), dim3(active * (p.I / 32)), dim3(256), lds,
+  hipLaunchKernelGGL((small_gate_up_kernel<NPL, TX>), dim3(active * (p.I / 32)), dim3(64 * kWaves), lds,
                      stream, p);
 }
 

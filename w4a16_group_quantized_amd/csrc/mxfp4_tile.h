@@ -261,22 +261,29 @@ __device__ __forceinline__ void store_scale(uint8_t* row, int blk, int blocks, i
 }
 
 // SiLU(gate) * up of a tile of 16 tokens x 32 columns of I, stored as MXFP4 (the
-// 32 columns are one block): waves 0 and 1 of 256 threads hold the gate's two
-// halves in acc, waves 2 and 3 the up's, lane (col, g) columns 4 g ... + 3 of
-// token col.  `h` is LDS of the workgroup.
-__device__ __forceinline__ void gate_up_epilogue(f32x4 acc, float (&h)[4][16][17], int wave, int I,
-                                                 int nt, int r0, int rows, uint8_t* act_codes,
-                                                 uint8_t* act_scales) {
+// 32 columns are one block): of each four waves, 0 and 1 hold the gate's two
+// halves in acc, 2 and 3 the up's, lane (col, g) columns 4 g ... + 3 of token col;
+// PARTS fours of waves hold parts of the sums.  `h` is LDS of the workgroup.
+template <int PARTS>
+__device__ __forceinline__ void gate_up_epilogue(f32x4 acc, float (&h)[4 * PARTS][16][17], int wave,
+                                                 int I, int nt, int r0, int rows,
+                                                 uint8_t* act_codes, uint8_t* act_scales) {
   const int col = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[wave][col][4 * g + i] = acc[i];
   __syncthreads();
+  if (threadIdx.x >= 256) return;
   // 16 threads per token, two neighbouring columns each
   const int t = threadIdx.x >> 4, c = (threadIdx.x & 15) * 2;
   float a[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const float gate = h[c >> 4][t][(c & 15) + q], up = h[2 + (c >> 4)][t][(c & 15) + q];
+    float gate = 0.f, up = 0.f;
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      gate += h[4 * p + (c >> 4)][t][(c & 15) + q];
+      up += h[4 * p + 2 + (c >> 4)][t][(c & 15) + q];
+    }
     a[q] = silu_mul(gate, up);
   }
   uint32_t m = max(abs_bits(a[0]), abs_bits(a[1]));
