@@ -620,7 +620,7 @@ size_t moe_mxfp4_layer_workspace_bytes(int64_t T, int32_t top_k, int32_t E,
  * from 5 tokens on the kernels are the calls' own).
  *
  *   logits      in   fp32 [T, E]
- *   x, out      in, out  dtype [T, H], dense
+ *   x, out      in, out  dtype [T, H], dense; out may be x
  *   w13_*       in   MXFP4 [E, 2I, H], rows [0, I) gate, [I, 2I) up
  *   w2_*        in   MXFP4 [E, H, I]
  *   workspace   scratch, device, >= moe_mxfp4_layer_workspace_bytes(...);
@@ -700,7 +700,9 @@ int moe_dispatch_backward(const void* grad_sorted, int32_t dtype, int64_t T,
  *   grad_y[slot_rows[s], :] = topk_weights[s] * grad_out[s / top_k, :]
  *   grad_weights[s] = sum_h grad_out[s / top_k, h] * y_sorted[slot_rows[s], h]
  * with 0 for a dropped slot; rows of grad_y that no slot points at are left
- * as they were.  grad_y must not overlap y_sorted or grad_out.
+ * as they were.  As for moe_dispatch, rows of distinct slots are distinct (a
+ * row that two slots hold would keep one slot's gradient, not their sum).
+ * grad_y must not overlap y_sorted or grad_out.
  *
  *   y_sorted      in   y_dtype [rows, H], stride y_stride
  *   topk_weights  in   fp32 [T, top_k]

@@ -517,6 +517,42 @@ def test_layer_in_a_graph_replayed(ops):
         assert torch.equal(out, _layer_steps(ops, logits, x, k, w)), f"replay {i}"
 
 
+@pytest.mark.parametrize("T", [1, 3, 100])
+def test_two_layers_in_a_graph_share_buffers(ops, T):
+    """Two layers in a row, the second reading the first's output, both with one workspace, replayed
+    with new inputs: the calls of a captured model step."""
+    rng = np.random.default_rng(T)
+    E, k, H, I = 40, 4, 192, 96
+    logits, x, w, _, _ = _layer_inputs(rng, T, E, H, I, torch.bfloat16)
+    more, _, w2, _, _ = _layer_inputs(rng, T, E, H, I, torch.bfloat16)
+    ws = torch.empty(ops.mxfp4_layer_workspace_bytes(T, k, E, H, I), dtype=torch.uint8, device="cuda")
+    mid, out = torch.empty_like(x), torch.empty_like(x)
+
+    def step(mid, out, ws):
+        ops.moe_mxfp4_layer_forward(logits, x, k, w, workspace=ws, out=mid)
+        ops.moe_mxfp4_layer_forward(more, mid, k, w2, workspace=ws, out=out)
+
+    step(mid, out, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(mid, out, ws)
+    for i in range(4):
+        logits.copy_(torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)))
+        x.copy_(torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)))
+        want = torch.empty_like(out)
+        step(torch.empty_like(mid), want, torch.empty_like(ws))
+        out.zero_()
+        ws.fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.isfinite(out).all(), f"replay {i}"
+    # a layer's output may take the place of its input
+    y = x.clone()
+    ops.moe_mxfp4_layer_forward(logits, y, k, w, out=y)
+    assert torch.equal(y, mid)
+
+
 def test_calls_follow_the_current_stream(ops):
     """Work on a side stream: the call waits for its inputs there, not on the default stream."""
     s = torch.cuda.Stream()

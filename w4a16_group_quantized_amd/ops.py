@@ -863,7 +863,7 @@ def moe_mxfp4_layer_forward(logits: torch.Tensor, x: torch.Tensor, top_k: int, w
     code = _DTYPE.get(dtype)
     if code is None:
         raise ValueError(f"x is {dtype}, not float32, float16 or bfloat16")
-    T = x.shape[0]
+    T = x.shape[0] if x.dim() == 2 else 0
     px, pl = _dense("x", x, dtype, T, H), _dense("logits", logits, torch.float32, T, E)
     if out is None:
         out = x.new_empty((T, H))
@@ -931,14 +931,14 @@ def moe_dispatch(x: torch.Tensor, slot_rows: torch.Tensor, top_k: int,
                  out: torch.Tensor | None = None) -> torch.Tensor:
     """Token rows to expert order: out[slot_rows[s]] = x[s // top_k].  out has T * top_k rows, or
     any number when given; rows that no slot points at are left as they were (zero when out is
-    made here)."""
+    made here).  No two slots may hold one row."""
     pr, T = _slots(slot_rows, top_k)
     px, dtype, sx, rows_x, H = _matrix("x", x)
     if rows_x != T:
         raise ValueError(f"x has {rows_x} rows, slot_rows {T} tokens")
     if out is None:
         out = x.new_zeros((T * top_k, H))
-    rows = out.shape[0]
+    rows = out.shape[0] if out.dim() == 2 else 0
     po, _, so = _sized("out", out, rows, H, dtype)
     _apart("out", out, x=x)
     _run("moe_dispatch", _device_of(x, slot_rows, out), px, dtype, T, top_k, H, sx, pr, rows, po, so)
@@ -981,7 +981,8 @@ def moe_combine_backward(grad_out: torch.Tensor, y_sorted: torch.Tensor,
                          topk_weights: torch.Tensor, slot_rows: torch.Tensor,
                          out: torch.Tensor | None = None, grad_weights: torch.Tensor | None = None):
     """moe_combine_masked's gradients: (grad_y of y_sorted's type and shape, grad_weights fp32
-    [T, top_k]).  Rows of grad_y that no slot points at are left as they were (zero when made here)."""
+    [T, top_k]).  Rows of grad_y that no slot points at are left as they were (zero when made here);
+    no two slots may hold one row."""
     pw, T, k = _weights(topk_weights)
     py, y_code, sy, rows, H = _matrix("y_sorted", y_sorted)
     pg, g_code, sg = _sized("grad_out", grad_out, T, H)
