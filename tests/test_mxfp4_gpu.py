@@ -382,6 +382,24 @@ def test_gate_up_of_few_rows_with_long_sums(ops, E, R, I, K):
     _check_act(*ops.moe_mxfp4_gate_up(_gpu(a[0]), _gpu(a[1]), _gpu(w[0]), _gpu(w[1]), _gpu(off)), h, size, I, K)
 
 
+@pytest.mark.parametrize("E,R,I,K", [(300, 9000, 96, 2080), (40, 4000, 448, 640), (70, 4900, 512, 352),
+                                     (500, 9000, 64, 96), (1, 3001, 2720, 160), (200, 2000, 160, 2080),
+                                     (1, 200, 96, 1600), (2, 70, 64, 224)])
+def test_gate_up_of_every_variant(ops, E, R, I, K):
+    """Each of the tiles' shapes, and few tiles, with odd ends; rows mapped."""
+    rng = np.random.default_rng(I)
+    a = _random_mx(rng, R, K, low=124, high=126)
+    w = _random_mx(rng, E, 2 * I, K, low=120, high=122)
+    off = _offsets(rng, E, R)
+    slots = rng.permutation(R).astype(np.int32)
+    h, size = ref.mx_product(ref.mx_values(*a), ref.mx_values(*w), off, slots)
+    args = (_gpu(a[0]), _gpu(a[1]), _gpu(w[0]), _gpu(w[1]), _gpu(off), _gpu(slots))
+    got = ops.moe_mxfp4_gate_up(*args)
+    _check_act(*got, h, size, I, K)
+    for x, y in zip(got, ops.moe_mxfp4_gate_up(*args)):
+        assert torch.equal(x, y)
+
+
 def test_gate_up_of_mapped_rows_leaves_other_rows_alone(ops):
     rng = np.random.default_rng(12)
     T, k, E, I, K = 30, 4, 6, 96, 160

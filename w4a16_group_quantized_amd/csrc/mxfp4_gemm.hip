@@ -34,6 +34,7 @@ namespace {
 // 512 experts, 1280 x 2560: 8.8 us for 17 MB (9.6 unsplit, 11.8 with the tiles
 // below, whose hundred workgroups leave half of the compute units idle).  Below
 // four windows the split costs: 20 experts, 2048 x 1280: 8.6 us (7.6 unsplit).
+// Gate/up in four shares is slower there (10.7) and 3 % faster for one long row.
 // Three windows in flight or five waves per SIMD are slower.
 constexpr int kTokens = 16;
 
@@ -658,9 +659,10 @@ void launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
   const bool light = mean <= 8 && weights <= 32 << 20;
   // products whose tiles would leave half of the compute units idle, stream /
   // tiles: 16384 x 16384, one row 30.5 / 48 us; 4096 x 4096, 48 rows 9.9 / 12.7;
-  // 512 x 512 x K 2048 7.2 / 9.1; 32768 x 4096, 16 rows (256 tiles) 23.5 / 15.1
+  // 512 x 512 x K 2048 7.2 / 9.1; 32768 x 4096, 16 rows (256 tiles) 23.5 / 15.1;
+  // gate/up 1280 x 2560, 40 rows 8.4 / 11.1; 4096 x 4096, 48 rows 12.7 / 13.5
   const int64_t tiles = static_cast<int64_t>(active) * ((mean + 15) / 16) * ((a.N + 127) / 128);
-  const bool few = a.act_codes == nullptr && tiles <= 128;
+  const bool few = tiles <= 128;
   // the split needs a window for each of four waves
   if (far || light || few) return launch_stream(a, !far && a.K > 1536, stream);
   // the tile that holds the mean, or a smaller one where its tiles would leave
