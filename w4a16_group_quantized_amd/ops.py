@@ -888,9 +888,9 @@ def moe_permute_masked(topk_ids: torch.Tensor, E: int, first_expert: int = 0,
     T, k = topk_ids.shape
     S = T * k
     if out is None:
-        out = {name: topk_ids.new_empty(n, dtype=torch.int32) for name, n in (
-            ("expert_offsets", E + 1), ("sorted_slots", S), ("slot_rows", S),
-            ("active_experts", E), ("num_active", 1))}
+        made = topk_ids.new_empty  # int32, or the ids are refused below
+        out = {"expert_offsets": made(E + 1), "sorted_slots": made(S), "slot_rows": made(S),
+               "active_experts": made(E), "num_active": made(1)}
         if T == 0:  # the call writes nothing then
             for name, fill in (("expert_offsets", 0), ("active_experts", -1), ("num_active", 0)):
                 out[name].fill_(fill)
