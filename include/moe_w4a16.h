@@ -616,8 +616,8 @@ size_t moe_mxfp4_layer_workspace_bytes(int64_t T, int32_t top_k, int32_t E,
  * quantised too: moe_route_permute, moe_mxfp4_quantize of x, moe_mxfp4_gate_up
  * over moe_permute's sorted_slots, moe_mxfp4_grouped_gemm into fp32 rows and
  * moe_combine_masked, in one call; out is what those calls produce up to the
- * order of the products' fp32 sums (up to 4 tokens two launches do all of it;
- * from 5 tokens on the kernels are the calls' own).
+ * order of the products' fp32 sums (up to 6 tokens two launches do all of it;
+ * from 7 tokens on the kernels are the calls' own).
  *
  *   logits      in   fp32 [T, E]
  *   x, out      in, out  dtype [T, H], dense; out may be x

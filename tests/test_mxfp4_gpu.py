@@ -477,6 +477,25 @@ def test_layer_is_its_calls_and_near_the_oracle(ops, T, E, k, H, I, dtype):
     assert np.sqrt((off ** 2).sum() / (want ** 2).sum()) <= 1e-2
 
 
+@pytest.mark.parametrize("dtype", DTYPES, ids=IDS)
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (5, 512, 10, 256, 64), (6, 1000, 10, 96, 32), (6, 4, 4, 160, 1088), (6, 8, 2, 16384, 32), (5, 1024, 12, 64, 544),
+    (4, 16, 16, 128, 1056), (6, 1, 1, 64, 2080), (2, 32, 32, 64, 96), (7, 64, 9, 128, 64), (6, 20, 11, 64, 64),
+])
+def test_layer_of_few_tokens_is_its_calls(ops, T, E, k, H, I, dtype):
+    """Around the two-launch form's limits (6 tokens, 64 slots, 1024 experts, 16384 columns): many
+    experts per wave, one or several windows of I, all slots on one expert, whole waves of slots."""
+    logits, x, w, w13, w2 = _layer_inputs(np.random.default_rng(T * E), T, E, H, I, dtype)
+    for same in (False, True):
+        if same:  # every token the same experts
+            logits[:] = logits[0].clone()
+        out = ops.moe_mxfp4_layer_forward(logits, x, k, w)
+        assert torch.equal(out, ops.moe_mxfp4_layer_forward(logits, x, k, w))
+        want = ref.mx_layer(logits.cpu().numpy(), _host(x), k, w13, w2)
+        for got in (out, _layer_steps(ops, logits, x, k, w)):
+            assert np.sqrt(((_host(got) - want) ** 2).sum() / (want ** 2).sum()) <= 1e-2
+
+
 def test_a_model_s_weights_through_the_layer(ops):
     """Float weights quantised at load time, expert by expert rows at once, then a decode and a
     prefill call on them."""

@@ -41,8 +41,8 @@ struct MxGemmArgs {
 void launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream);
 
 // The whole layer for a few tokens, in two launches (mxfp4_small.hip).
-constexpr int kMxSmallTokens = 4;
-constexpr int kMxSmallHidden = 16384;  // 4 tokens of quantised x in LDS: 34 KB
+constexpr int kMxSmallTokens = 6;
+constexpr int kMxSmallHidden = 16384;  // 6 tokens of quantised x in LDS: 51 KB
 struct MxSmallArgs {
   const float* logits;
   const void* x;

@@ -1,11 +1,11 @@
-// The MXFP4 layer for one to four tokens in two launches.
+// The MXFP4 layer for one to six tokens in two launches.
 //
 // With so few tokens the five launches of the layer's steps (router and
 // permutation, quantisation, gate/up, down, combine) are latency: 33.6 us at one
 // token of 512 experts, 10 chosen, hidden 2560, intermediate 640, for 26 MB of
-// weights; 19.3 us in these two (28 against 44 at two tokens, 49 against 60 at
-// four, 64 against 67 at five, which is left to the others).  Here every
-// workgroup does the small steps for itself:
+// weights; 17.4 us in these two (24 against 44 at two tokens, 41 against 60 at
+// four, 52 against 63 at five, 64 against 73 at six).  Here every workgroup does
+// the small steps for itself:
 //   gate/up  routes the tokens (one wave each) while its other waves quantise
 //            them into LDS, then takes 32 columns of I of one expert, as the
 //            streaming product does
@@ -20,7 +20,6 @@ namespace {
 
 constexpr int kMaxSlots = 64;  // one slot per lane
 constexpr int kMaxTokens = kMxSmallTokens;
-static_assert(kMaxTokens <= 4, "a wave per token");
 
 // The permutation of at most 64 slots, lane s holding slot s (id < 0: none):
 // the slot's row (slots ascending by expert, then by slot), and the ordinal of
@@ -30,20 +29,15 @@ struct Places {
 };
 __device__ __forceinline__ Places place_slots(int id, int S) {
   const int lane = threadIdx.x & 63;
+  // distinct keys below 2^31: experts are fewer than 2^24
+  const int key = lane < S ? id * 64 + lane : INT32_MAX;
   int row = 0;
-  bool first = true;
-  for (int q = 0; q < S; ++q) {
-    const int other = __builtin_amdgcn_readlane(id, q);
-    row += other < id || (other == id && q < lane);
-    first &= !(other == id && q < lane);
-  }
-  unsigned long long firsts = __ballot(first && lane < S);
-  int ordinal = 0;
-  while (firsts) {
-    const int q = __builtin_ctzll(firsts);
-    firsts &= firsts - 1;
-    ordinal += __builtin_amdgcn_readlane(id, q) < id;
-  }
+  for (int q = 0; q < S; ++q) row += __builtin_amdgcn_readlane(key, q) < key;
+  // the ids in the order of rows: an expert starts where they change
+  const int sorted = __builtin_amdgcn_ds_permute(row * 4, id);
+  const int before = __shfl_up(sorted, 1);  // in all lanes, the comparison's branch behind it
+  const unsigned long long firsts = __ballot(lane < S && (lane == 0 || sorted != before));
+  const int ordinal = __popcll(firsts & ((2ull << row) - 1)) - 1;
   return {row, ordinal};
 }
 
@@ -135,8 +129,8 @@ __device__ __forceinline__ void load_window(WeightWindow& b, const Weights& w, i
   }
 }
 
-// acc += the window's products; row(blk) gives the token's block, word(blk) the
-// scale word that holds blocks blk ... blk + 3.
+// acc += the window's products; row(i, blk) gives the token's block of step i,
+// word(i, blk) the scale word that holds blocks blk ... blk + 3.
 template <typename Row, typename Word>
 __device__ __forceinline__ void multiply_window(f32x4& acc, const WeightWindow& b, int win,
                                                 int blocks, Row&& row, Word&& word) {
@@ -147,8 +141,8 @@ __device__ __forceinline__ void multiply_window(f32x4& acc, const WeightWindow& 
     if (blk >= blocks) return;
     const bool in = blk + g < blocks;  // blocks behind K are zeros of scale 1
     const uint32_t sw = in ? b.s[i] >> (8 * g) : 127u;
-    const uint32_t sa = in ? word(blk) >> (8 * g) : 127u;
-    const dwords4 a = in ? row(blk + g) : dwords4{};
+    const uint32_t sa = in ? word(i, blk) >> (8 * g) : 127u;
+    const dwords4 a = in ? row(i, blk + g) : dwords4{};
     acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(b.w[i]), operand(a), acc, kFp4,
                                                            kFp4, 0, sw, 0, sa);
   }
@@ -158,8 +152,9 @@ constexpr int kInFlight = 2;  // windows; four or six are slower (22.2, 22.6 aga
 
 // ---- gate/up -------------------------------------------------------------------
 // K is shared out to the waves in windows, kParts fours of waves per workgroup: one
-// token 19.3 us (19.9 in one share, 19.8 in four), four tokens 49 (50, 60).
+// or four shares cost one token half a microsecond, four shares four tokens ten.
 constexpr int kParts = 2, kWaves = 4 * kParts;
+constexpr int kQuantWords = 2;  // words per lane whose loads are in flight (six tokens: 67 us with one)
 
 template <int NPL, typename TX>
 __global__ __launch_bounds__(64 * kWaves) void small_gate_up_kernel(MxSmallArgs p) {
@@ -196,21 +191,29 @@ __global__ __launch_bounds__(64 * kWaves) void small_gate_up_kernel(MxSmallArgs 
   static_assert(kWaves > kMaxTokens, "some wave quantises");
   if (wave >= q0) {
     const int words = p.H / 8, total = p.T * words, step = (kWaves - q0) * 64;
-    for (int i0 = (wave - q0) * 64; i0 < total; i0 += step) {
-      const int i = min(i0 + lane, total - 1);  // whole blocks: total is a multiple of 4
-      const int t = i / words, c = i - t * words;
-      float v[8];
-      load8<TX>(static_cast<const typename TX::bits*>(p.x) + static_cast<size_t>(t) * p.H + 8 * c,
-                8, v);
-      uint32_t m = 0;
+    for (int i0 = (wave - q0) * 64; i0 < total; i0 += step * kQuantWords) {
+      float v[kQuantWords][8];
+      int t[kQuantWords], c[kQuantWords];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) m = max(m, abs_bits(v[q]));
-      m = quad_max<0xB1>(m);
-      m = quad_max<0x4E>(m);
-      const uint32_t byte = mx_scale_byte(m);
-      if (i0 + lane < total) {
-        *reinterpret_cast<uint32_t*>(codes + t * (p.H / 2) + 4 * c) = mx_word(v, byte);
-        if ((c & 3) == 0) scales[t * sbytes + (c >> 2)] = static_cast<uint8_t>(byte);
+      for (int u = 0; u < kQuantWords; ++u) {
+        const int i = min(i0 + u * step + lane, total - 1);  // whole blocks: total is a multiple of 4
+        t[u] = i / words, c[u] = i - t[u] * words;
+        load8<TX>(
+            static_cast<const typename TX::bits*>(p.x) + static_cast<size_t>(t[u]) * p.H + 8 * c[u], 8,
+            v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kQuantWords; ++u) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m = max(m, abs_bits(v[u][q]));
+        m = quad_max<0xB1>(m);
+        m = quad_max<0x4E>(m);
+        const uint32_t byte = mx_scale_byte(m);
+        if (i0 + u * step + lane < total) {
+          *reinterpret_cast<uint32_t*>(codes + t[u] * (p.H / 2) + 4 * c[u]) = mx_word(v[u], byte);
+          if ((c[u] & 3) == 0) scales[t[u] * sbytes + (c[u] >> 2)] = static_cast<uint8_t>(byte);
+        }
       }
     }
   }
@@ -237,10 +240,10 @@ __global__ __launch_bounds__(64 * kWaves) void small_gate_up_kernel(MxSmallArgs 
   const int token = left ? __builtin_ctzll(left) / p.top_k : -1;
   const uint8_t* my_codes = codes + max(token, 0) * (p.H / 2);
   const uint8_t* my_scales = scales + max(token, 0) * sbytes;
-  auto row = [&](int blk) {
+  auto row = [&](int, int blk) {
     return token >= 0 ? *reinterpret_cast<const dwords4*>(my_codes + blk * 16) : dwords4{};
   };
-  auto word = [&](int blk) -> uint32_t {
+  auto word = [&](int, int blk) -> uint32_t {
     return token >= 0 ? *reinterpret_cast<const uint32_t*>(my_scales + blk) : 0x7F7F7F7Fu;
   };
 
@@ -261,7 +264,35 @@ __global__ __launch_bounds__(64 * kWaves) void small_gate_up_kernel(MxSmallArgs 
 }
 
 // ---- down and combine --------------------------------------------------------------
-constexpr int kDownWaves = 16;
+// Without registers to spill: 16 waves are held to 128 each, and one token then
+// takes 26 us instead of 18.6 (8 or 10 waves 18.6).
+constexpr int kDownWaves = 12;
+
+// A wave's windows of one expert after another are one sequence, two of them in
+// flight with the rows they meet, so that no expert starts from an empty pipe.
+struct DownExpert {
+  Weights w;  // no blocks: none left, loads give zeros
+  const uint8_t *codes, *scales;
+  int r0, count;  // its rows
+};
+struct DownWindow {
+  WeightWindow w;
+  dwords4 a[4];
+  uint32_t s[4];
+};
+__device__ __forceinline__ void load_window(DownWindow& b, const DownExpert& x, int win) {
+  const int col = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+  load_window(b.w, x.w, win);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int blk = win * 16 + 4 * i;
+    b.a[i] = dwords4{};
+    b.s[i] = 127u * 0x01010101u;
+    if (col >= x.count) continue;
+    if (blk + g < x.w.blocks) b.a[i] = *reinterpret_cast<const dwords4*>(x.codes + (blk + g) * 16);
+    if (blk < x.w.blocks) b.s[i] = *reinterpret_cast<const uint32_t*>(x.scales + blk);
+  }
+}
 
 template <typename TO>
 __global__ __launch_bounds__(64 * kDownWaves) void small_down_kernel(MxSmallArgs p) {
@@ -277,41 +308,51 @@ __global__ __launch_bounds__(64 * kDownWaves) void small_down_kernel(MxSmallArgs
   const int col = lane & 15, g = lane >> 4;
   const int n = blockIdx.x * 16 + col;
   const int windows = (blocks + 15) / 16;
-  for (int x = wave;; x += kDownWaves) {
+  auto expert = [&](int x) {
     const unsigned long long mine = slots_of(at, S, x);
-    if (mine == 0) break;
-    const int lead = __builtin_ctzll(mine);
-    const int e = __builtin_amdgcn_readlane(id, lead), r0 = __builtin_amdgcn_readlane(at.row, lead);
-    const bool live = col < __popcll(mine);
-    const int64_t r = live ? r0 + col : r0;
-    const Weights w{
-        make_rsrc(p.w2_codes + static_cast<int64_t>(e) * p.H * (p.I / 2),
-                  static_cast<uint32_t>(p.H) * (p.I / 2)),
-        make_rsrc(p.w2_scales + static_cast<int64_t>(e) * p.H * sbytes,
-                  static_cast<uint32_t>(p.H) * sbytes),
-        static_cast<uint32_t>(n) * (p.I / 2), static_cast<uint32_t>(n) * sbytes, blocks};
-    const uint8_t* my_codes = p.act_codes + r * (p.I / 2);
-    const uint8_t* my_scales = p.act_scales + r * sbytes;
-    auto row = [&](int blk) {
-      return live ? *reinterpret_cast<const dwords4*>(my_codes + blk * 16) : dwords4{};
-    };
-    auto word = [&](int blk) -> uint32_t {
-      return live ? *reinterpret_cast<const uint32_t*>(my_scales + blk) : 0x7F7F7F7Fu;
-    };
-    WeightWindow b[2];
-    load_window(b[0], w, 0);
-    load_window(b[1], w, 1);
+    const int lead = mine ? __builtin_ctzll(mine) : 0;
+    const int e = mine ? __builtin_amdgcn_readlane(id, lead) : 0;
+    DownExpert q;
+    q.r0 = __builtin_amdgcn_readlane(at.row, lead);
+    q.count = __popcll(mine);
+    const int r = q.r0 + (col < q.count ? col : 0);
+    q.w = {make_rsrc(p.w2_codes + static_cast<int64_t>(e) * p.H * (p.I / 2),
+                     static_cast<uint32_t>(p.H) * (p.I / 2)),
+           make_rsrc(p.w2_scales + static_cast<int64_t>(e) * p.H * sbytes,
+                     static_cast<uint32_t>(p.H) * sbytes),
+           static_cast<uint32_t>(n) * (p.I / 2), static_cast<uint32_t>(n) * sbytes,
+           mine ? blocks : 0};
+    q.codes = p.act_codes + static_cast<int64_t>(r) * (p.I / 2);
+    q.scales = p.act_scales + static_cast<int64_t>(r) * sbytes;
+    return q;
+  };
+  auto multiply = [&](f32x4& acc, const DownWindow& b, int win) {
+    multiply_window(acc, b.w, win, blocks, [&](int i, int) { return b.a[i]; },
+                    [&](int i, int) { return b.s[i]; });
+  };
+  DownExpert now = expert(wave);
+  DownWindow b[2];
+  load_window(b[0], now, 0);
+  load_window(b[1], now, 1);
+  for (int x = wave + kDownWaves; now.count > 0; x += kDownWaves) {
+    const DownExpert next = expert(x);
     f32x4 acc{};
-    for (int win = 0; win < windows; win += 2) {
-      multiply_window(acc, b[0], win, blocks, row, word);
-      load_window(b[0], w, win + 2);
-      if (win + 1 < windows) multiply_window(acc, b[1], win + 1, blocks, row, word);
-      load_window(b[1], w, win + 3);
+    int win = 0;
+    for (; win + 2 < windows; win += 2) {
+      multiply(acc, b[0], win);
+      load_window(b[0], now, win + 2);
+      multiply(acc, b[1], win + 1);
+      load_window(b[1], now, win + 3);
     }
-    if (live) {
+    multiply(acc, b[0], win);
+    load_window(b[0], next, 0);
+    multiply(acc, b[1], win + 1);  // nothing if there is none
+    load_window(b[1], next, 1);
+    if (col < now.count) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[r0 + col][4 * g + i] = acc[i];
+      for (int i = 0; i < 4; ++i) y[now.r0 + col][4 * g + i] = acc[i];
     }
+    now = next;
   }
   __syncthreads();
   const int t = threadIdx.x >> 4, c = threadIdx.x & 15;
