@@ -1,0 +1,147 @@
+"""GPU: the MXFP4 and row calls where ordinary inputs do not lead."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from oracle import mxfp4_oracle as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def ops():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from w4a16_group_quantized_amd import ops
+
+    ops.load_library()
+    return ops
+
+
+@pytest.fixture(autouse=True)
+def _announce(request):
+    print(f"\n[gpu-test] {request.node.nodeid}", flush=True)
+    yield
+
+
+def _gpu(a: np.ndarray) -> torch.Tensor:
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _host(t: torch.Tensor) -> np.ndarray:
+    return (t.float() if t.is_floating_point() else t).cpu().numpy()
+
+
+def _mx(values: np.ndarray, bytes_: np.ndarray):
+    """Packed rows [..., K] of E2M1 values with the given scale bytes [..., K/32] (padding 255)."""
+    K = values.shape[-1]
+    flat = values.reshape(-1, K)
+    code = np.abs(np.abs(flat)[..., None] - ref.E2M1).argmin(axis=-1) + 8 * np.signbit(flat)
+    assert np.array_equal(ref.E2M1[code & 7], np.abs(flat))
+    words, scales = ref.mx_pack(code.astype(np.uint8), bytes_.reshape(len(flat), -1).astype(np.uint8))
+    scales[:, K // 32:] = 255
+    return (words.reshape(*values.shape[:-1], -1), scales.reshape(*values.shape[:-1], -1))
+
+
+# ---- SiLU over the whole of fp32 ------------------------------------------------------
+# each gate is a 2^p + b 2^q, exact in fp32: about 17, 84, 88, 120, 1e30, 2.3e38, 2.4e38, 3.2e38
+_GATES = [(1.0, 4, 1.0, 0), (1.5, 6, -1.5, 3), (1.0, 6, 1.5, 4), (1.0, 7, -1.0, 3), (1.5, 99, 0.0, 0),
+          (1.5, 127, -1.0, 124), (1.5, 127, -1.0, 123), (1.5, 127, 1.5, 125)]
+
+
+def _wide_gates(K: int):
+    """(W13 [1, 2I, K] as MXFP4, gates [I], ups [I]) whose sums over a row with ones at columns 0 and
+    32 are the gates of both signs, 32 columns each, and small ups."""
+    I = 64 * len(_GATES)
+    values, bytes_ = np.zeros((2 * I, K)), np.full((2 * I, K // 32), 127)
+    ups = np.resize([0.5, 1.0, -1.5, 2.0, 3.0, -4.0], I)
+    for i, (a, p, b, q) in enumerate(_GATES):
+        for half, sign in enumerate((1.0, -1.0)):
+            at = slice(64 * i + 32 * half, 64 * i + 32 * half + 32)
+            values[at, 0], values[at, 32] = sign * a, sign * b
+            bytes_[at, 0], bytes_[at, 1] = p + 127, q + 127
+    values[I:, 0] = ups
+    bytes_[I:, 0] = 127 - 20
+    w = _mx(values[None], bytes_[None])
+    h = ref.mx_values(*w)[0].sum(axis=1)
+    return w, h[:I], h[I:]
+
+
+def _silu_mul(gate: np.ndarray, up: np.ndarray):
+    """SiLU(gate) * up in fp64, and what fp32 may be off by: a few roundings of the value (exponential,
+    sum, quotient, two products), and a reciprocal below 2^-126 that counts as zero."""
+    with np.errstate(over="ignore"):
+        act = gate / (1.0 + np.exp(-gate)) * up
+    return act, 8 * 2.0 ** -24 * np.abs(act) + 2.0 ** -126 * np.abs(gate * up)
+
+
+@pytest.mark.parametrize("R,K", [(3, 64), (3, 1600), (900, 64)], ids=["stream", "stream-split", "tile"])
+def test_gate_up_over_the_whole_range_of_gates(ops, R, K):
+    w, gate, up = _wide_gates(K)
+    ones = np.zeros((R, K))
+    ones[:, [0, 32]] = 1.0
+    a = _mx(ones, np.full((R, K // 32), 127))
+    codes, scales = ops.moe_mxfp4_gate_up(_gpu(a[0]), _gpu(a[1]), _gpu(w[0]), _gpu(w[1]))
+    I = len(gate)
+    act, err = _silu_mul(gate, up)
+    b = _host(scales)[:, : I // 32].astype(np.int64)
+    top, off = np.abs(act).reshape(-1, 32), err.reshape(-1, 32)
+    lo = ref.mx_exponent(np.maximum(top - off, 0).max(axis=1)) + 127
+    hi = ref.mx_exponent((top + off).max(axis=1)) + 127
+    assert ((lo <= b) & (b <= hi)).all(), (lo, hi, b[0])
+    got = ref.mx_values(_host(codes), _host(scales))
+    unit = np.repeat(np.exp2(b - 127.0), 32, axis=1)
+    m = (np.abs(act) + err) / unit
+    half = np.where(m <= 2, 0.25, np.where(m <= 4, 0.5, np.maximum(1.0, m - 6)))
+    assert (np.abs(got - act) <= half * unit + err).all()
+
+
+def test_gate_up_keeps_nan_and_infinite_gates(ops):
+    """A NaN sum, and one past fp32: blocks of scale byte 255 and zero codes, in each kernel form."""
+    for R in (3, 900):
+        for value, byte in ((1.0, 255), (6.0, 254)):
+            K, I = 64, 96
+            v, s = np.zeros((1, 2 * I, K)), np.full((1, 2 * I, K // 32), 127)
+            v[0, :, 0] = 1.0
+            v[0, 40, 0], s[0, 40, 0] = value, byte  # gate 40, in the second block
+            ones = np.zeros((R, K))
+            ones[:, 0] = 1.0
+            w, a = _mx(v, s), _mx(ones, np.full((R, K // 32), 127))
+            codes, scales = ops.moe_mxfp4_gate_up(*(_gpu(t) for t in (*a, *w)))
+            codes, scales = _host(codes), _host(scales)
+            assert (scales[:, 1] == 255).all() and (codes[:, 4:8] == 0).all(), (R, byte)
+            assert (scales[:, [0, 2]] != 255).all() and (codes[:, :4] != 0).all(), (R, byte)
+
+
+@pytest.mark.parametrize("T", [1, 6, 7, 90])
+def test_layer_over_the_whole_range_of_gates(ops, T):
+    """The layer's gate/up, in its form for few tokens and in the calls' own: outputs of every gate
+    apart (w2 picks one column of I each, its scale brings the product back to about 1)."""
+    H = K = 64
+    w13, gate, up = _wide_gates(K)
+    I = len(gate)
+    act, err = _silu_mul(gate, up)
+    got_bytes = ref.mx_exponent(np.abs(act).reshape(-1, 32).max(axis=1))
+    values, bytes_ = np.zeros((1, H, I)), np.full((1, H, I // 32), 127)
+    picks = np.arange(H) * (I // H) + np.arange(H) % 7
+    big = np.abs(act[picks]) > 2.0 ** -100
+    for n, i in enumerate(picks):
+        values[0, n, i] = 1.0
+        bytes_[0, n, i // 32] = 127 - max(min(int(got_bytes[i // 32]), 127), -100)
+    w2 = _mx(values, bytes_)
+    x = torch.zeros(T, H, device="cuda")
+    x[:, [0, 32]] = 1.0
+    logits = torch.zeros(T, 1, device="cuda")
+    w = {"w13_codes": _gpu(w13[0]), "w13_scales": _gpu(w13[1]), "w2_codes": _gpu(w2[0]), "w2_scales": _gpu(w2[1])}
+    out = _host(ops.moe_mxfp4_layer_forward(logits, x, 1, w)).astype(np.float64)
+    scale = ref.mx_values(*w2)[0][np.arange(H), picks]
+    want = act[picks] * scale
+    # an act is stored with half an E2M1 step of its block, at most 1 unit below 6 and 2 behind
+    unit = np.exp2(got_bytes[picks // 32].astype(np.float64)) * scale
+    assert np.isfinite(out).all()
+    assert (np.abs(out - want)[:, big] <= (2.0 * unit + err[picks] * scale)[big]).all()
+    assert (np.abs(out[:, big]) > 0).any(axis=0).sum() >= 24

@@ -207,13 +207,18 @@ __device__ __forceinline__ void store4(typename T::bits* p, int n, f32x4 v) {
 // ---- the quantising epilogue ---------------------------------------------------
 // gate / (1 + e^-gate) * up in a dozen instructions (the library's exponential
 // and division made the epilogue the longest part of the gate/up product).
-// e^-gate = 2^t (1 + r ln 2), t = -gate log2(e) rounded and r what that rounding
-// left, so the exponential is good to 2 units in the last place at any gate;
-// the hardware's reciprocal to 1.
+// With x = -gate, e^x = 2^t (1 + r ln 2), t = x log2(e) rounded and r what that
+// rounding left, so the exponential is good to 2 units in the last place while it
+// is a normal number, the hardware's reciprocal to 1 down to 2^-126.  x is held in
+// [-128, 128], outside which e^x is 0 or past fp32 anyway: t of a finite gate past
+// 2.3e38 would be infinite and r with it, and 0 times r a NaN.  Below a gate of
+// -87.3 the reciprocal is under 2^-126 and counts as 0: what is lost is under
+// 2^-126 |gate up|.  A NaN gate stays NaN through the last product.
 __device__ __forceinline__ float silu_mul(float gate, float up) {
   constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147181f;
-  const float t = -gate * kLog2e;
-  const float r = fmaf(-gate, kLog2eRest, fmaf(-gate, kLog2e, -t));
+  const float x = __builtin_amdgcn_fmed3f(-gate, -128.f, 128.f);
+  const float t = x * kLog2e;
+  const float r = fmaf(x, kLog2eRest, fmaf(x, kLog2e, -t));
   const float e = __builtin_amdgcn_exp2f(t) * fmaf(r, kLn2, 1.f);
   return gate * __builtin_amdgcn_rcpf(1.f + e) * up;
 }
