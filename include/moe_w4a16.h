@@ -565,10 +565,10 @@ int moe_mxfp4_dequantize(const int32_t* codes, const uint8_t* scales,
  *                                for expert_offsets[e] <= r < expert_offsets[e+1]
  * Products are exact, summed in fp32, rounded once to out_dtype.  a(r) = r, or
  * row_slots[r] / top_k when row_slots is given (moe_permute's sorted_slots:
- * the rows of the tokens, without a copy in expert order); a slot outside
- * [0, a_rows * top_k) takes a row of zeros.  Rows outside
- * [expert_offsets[0], expert_offsets[E]) are left as they were.  A NaN scale
- * makes every sum that it enters NaN.
+ * the rows of the tokens, without a copy in expert order); the row of a slot
+ * outside [0, a_rows * top_k) is zeros, whatever the weights hold.  Rows
+ * outside [expert_offsets[0], expert_offsets[E]) are left as they were.  A NaN
+ * scale makes every sum that it enters NaN.
  *
  *   a_codes, a_scales  in   MXFP4 [a_rows, K]
  *   row_slots          in   int32 [rows], or NULL (then rows <= a_rows)

@@ -145,3 +145,36 @@ def test_layer_over_the_whole_range_of_gates(ops, T):
     assert np.isfinite(out).all()
     assert (np.abs(out - want)[:, big] <= (2.0 * unit + err[picks] * scale)[big]).all()
     assert (np.abs(out[:, big]) > 0).any(axis=0).sum() >= 24
+
+
+# ---- rows without a token ---------------------------------------------------------------
+ABSENT = [  # rows of A, top_k, E, N, K: streaming, K shared out, and tiles
+    (23, 3, 5, 128, 416), (9, 2, 2, 128, 1600), (1500, 3, 40, 896, 640), (2150, 2, 2, 4160, 288), (300, 4, 64, 192, 1120),
+]
+
+
+@pytest.mark.parametrize("T,k,E,N,K", ABSENT)
+def test_a_row_without_a_token_is_zero_whatever_the_weights_hold(ops, T, k, E, N, K):
+    rng = np.random.default_rng(T)
+    S = T * k
+    words = lambda *s: rng.integers(0, 1 << 32, size=(*s, K // 8), dtype=np.uint32).view(np.int32)
+    a = words(T), np.full((T, ref.mx_scale_bytes(K)), 125, np.uint8)
+    w = words(E, N), np.full((E, N, ref.mx_scale_bytes(K)), 121, np.uint8)
+    w[1][:, 17, 1] = 255  # column 17 of every expert
+    slots = rng.permutation(S).astype(np.int32)
+    gone = rng.random(S) < 0.2
+    gone[[0, S - 1]] = True
+    slots[gone] = rng.choice([-1, S, S + 5, -(1 << 31), (1 << 31) - 1], size=int(gone.sum()))
+    off = np.sort(np.concatenate([[0, S], rng.integers(0, S + 1, E - 1)])).astype(np.int32)
+    args = [_gpu(t) for t in (*a, *w, off)]
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.full((S, N), 7.0, device="cuda", dtype=dtype)
+        got = _host(ops.moe_mxfp4_grouped_gemm(*args, row_slots=_gpu(slots), top_k=k, out=out))
+        assert (got[gone] == 0).all()
+        assert np.isnan(got[~gone][:, 17]).all() and np.isnan(got).sum() == (~gone).sum()
+    codes, scales = ops.moe_mxfp4_gate_up(*args, row_slots=_gpu(slots), top_k=k)
+    codes, scales = _host(codes), _host(scales)
+    blocks = N // 64
+    assert (codes[gone] == 0).all() and (scales[gone][:, :blocks] == 0).all()
+    assert (scales[~gone][:, 0] == 255).all() and (codes[~gone][:, :4] == 0).all()
+    assert (scales[:, 1:blocks] != 255).all()

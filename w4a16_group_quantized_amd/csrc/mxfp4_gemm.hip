@@ -125,7 +125,9 @@ __global__ __launch_bounds__(GATE_UP ? 256 * SPLIT : 256) void mx_stream_kernel(
     load(b1, w + 3 * SPLIT);
   }
 
-  // acc[i] is column n0 + 4 g + i of token r0 + col
+  // acc[i] is column n0 + 4 g + i of token r0 + col.  A row without a token is zeros
+  // whatever the weights hold (its zeros times a NaN scale are NaN)
+  if (arow < 0) acc = f32x4{};
   if constexpr (GATE_UP) {
     __shared__ float h[4 * SPLIT][16][17];
     gate_up_epilogue<SPLIT>(acc, h, wave, I, nt, r0, r1 - r0, p.act_codes, p.act_scales);
