@@ -25,7 +25,8 @@ int check_launch() {
 int check_routing(int64_t T, int32_t top_k, int32_t E) {
   if (T < 0 || E < 1 || top_k < 1 || top_k > E) return MOE_ERR_INVALID_ARG;
   if (E > kMaxExperts || top_k > kMaxTopK) return MOE_ERR_UNSUPPORTED;
-  if (T * static_cast<int64_t>(top_k) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  // T by itself first: the product of a larger one could pass 64 bits
+  if (T > INT32_MAX || T * top_k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -52,7 +53,7 @@ int check_mfma(const Plan& pl, int64_t T, int32_t top_k, int32_t E, int32_t H, i
 int check_router_gate(int64_t T, int32_t H, int32_t E) {
   if (T < 0 || E < 1 || H <= 0 || H % kGroup) return MOE_ERR_INVALID_ARG;
   if (E > kMaxExperts || H / kGroup > kMaxGroups) return MOE_ERR_UNSUPPORTED;
-  if (T * static_cast<int64_t>(H) * 2 >= (static_cast<int64_t>(1) << 32)) return MOE_ERR_UNSUPPORTED;
+  if (T > INT32_MAX || T * H * 2 >= (static_cast<int64_t>(1) << 32)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -386,7 +387,7 @@ int moe_combine(const float* y_sorted, const float* topk_weights, const int32_t*
                 int64_t T, int32_t top_k, int32_t H, uint16_t* out, void* stream) {
   if (T < 0 || top_k < 1 || top_k > kMaxTopK) return top_k > kMaxTopK ? MOE_ERR_UNSUPPORTED
                                                                         : MOE_ERR_INVALID_ARG;
-  if (T * static_cast<int64_t>(top_k) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (T > INT32_MAX || T * top_k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (H <= 0 || H % kGroup) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!ok_ptr(y_sorted) || !ok_ptr(topk_weights) || !ok_ptr(slot_rows) || !ok_ptr(out))

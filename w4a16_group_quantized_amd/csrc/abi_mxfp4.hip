@@ -41,7 +41,8 @@ int check_mx(int64_t rows, int32_t K) {
 // limit (a token may hold fewer distinct ones than E).
 int check_slots(int64_t T, int32_t top_k) {
   if (T < 0 || top_k < 1) return MOE_ERR_INVALID_ARG;
-  if (top_k > kMaxTopK || T * static_cast<int64_t>(top_k) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  // T by itself first: the product of a larger one could pass 64 bits
+  if (top_k > kMaxTopK || T > INT32_MAX || T * top_k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
