@@ -178,3 +178,16 @@ def test_a_row_without_a_token_is_zero_whatever_the_weights_hold(ops, T, k, E, N
     assert (codes[gone] == 0).all() and (scales[gone][:, :blocks] == 0).all()
     assert (scales[~gone][:, 0] == 255).all() and (codes[~gone][:, :4] == 0).all()
     assert (scales[:, 1:blocks] != 255).all()
+
+
+# ---- an empty batch -----------------------------------------------------------------------
+def test_permutation_of_no_tokens_into_given_buffers(ops):
+    """A batch without tokens after one with some, both into the same buffers."""
+    E, k = 6, 2
+    out = ops.moe_permute_masked(torch.tensor([[1, 5], [1, 0]], dtype=torch.int32, device="cuda"), E)
+    out["sorted_slots"], out["slot_rows"] = out["sorted_slots"][:0], out["slot_rows"][:0]
+    ids = torch.empty(0, k, dtype=torch.int32, device="cuda")
+    want = {n: torch.from_numpy(v) for n, v in ref.permute_masked(np.zeros((0, k), np.int32), E).items()}
+    for got in (ops.moe_permute_masked(ids, E, out=out), ops.moe_permute_masked(ids, E)):
+        for name, value in want.items():
+            assert torch.equal(got[name].cpu(), value), name

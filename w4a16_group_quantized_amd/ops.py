@@ -882,7 +882,8 @@ def permute_masked_workspace_bytes(T: int, top_k: int, E: int) -> int:
 def moe_permute_masked(topk_ids: torch.Tensor, E: int, first_expert: int = 0,
                        workspace: torch.Tensor | None = None, out: dict | None = None) -> dict:
     """moe_permute for ids that may leave slots out: an id outside [first_expert, first_expert + E)
-    drops its slot (slot_rows -1); sorted_slots ends with -1 for each dropped slot."""
+    drops its slot (slot_rows -1); sorted_slots ends with -1 for each dropped slot.  No tokens
+    give empty segments, in buffers given too."""
     if topk_ids.dim() != 2:
         raise ValueError(f"topk_ids has shape {tuple(topk_ids.shape)}, not [T, top_k]")
     T, k = topk_ids.shape
@@ -891,9 +892,6 @@ def moe_permute_masked(topk_ids: torch.Tensor, E: int, first_expert: int = 0,
         made = topk_ids.new_empty  # int32, or the ids are refused below
         out = {"expert_offsets": made(E + 1), "sorted_slots": made(S), "slot_rows": made(S),
                "active_experts": made(E), "num_active": made(1)}
-        if T == 0:  # the call writes nothing then
-            for name, fill in (("expert_offsets", 0), ("active_experts", -1), ("num_active", 0)):
-                out[name].fill_(fill)
     if workspace is None:
         need = permute_masked_workspace_bytes(T, k, E)
         if need:
@@ -906,6 +904,9 @@ def moe_permute_masked(topk_ids: torch.Tensor, E: int, first_expert: int = 0,
          _dense("sorted_slots", slots, torch.int32, S), _dense("slot_rows", rows, torch.int32, S),
          _dense("active_experts", active, torch.int32, E),
          _dense("num_active", count, torch.int32, 1), *_bytes("workspace", workspace))
+    if T == 0:  # the call writes nothing then
+        for t, value in ((offsets, 0), (active, -1), (count, 0)):
+            t.fill_(value)
     return out
 
 
