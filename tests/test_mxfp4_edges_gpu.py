@@ -191,3 +191,22 @@ def test_permutation_of_no_tokens_into_given_buffers(ops):
     for got in (ops.moe_permute_masked(ids, E, out=out), ops.moe_permute_masked(ids, E)):
         for name, value in want.items():
             assert torch.equal(got[name].cpu(), value), name
+
+
+# ---- scales at the ends of their range --------------------------------------------------
+@pytest.mark.parametrize("E,R,N,K", [(1, 3, 48, 96), (1, 3, 48, 1600), (1, 900, 300, 288), (3, 800, 300, 1088)],
+                         ids=["stream", "stream-split", "tile", "tile-long"])
+@pytest.mark.parametrize("a_byte,w_byte", [(0, 254), (254, 0), (0, 127), (127, 0), (0, 140), (254, 100), (0, 0)])
+def test_product_with_scale_bytes_0_and_254(ops, E, R, N, K, a_byte, w_byte):
+    """Terms are multiples of 2^-2 of the scales' product, at most 36 of it.  Where that product is a
+    normal number the bound is the usual one, K fp32 roundings; at byte 0 against 127 every sum is a
+    multiple of 2^-129, which fp32 holds exactly up to 2^-105."""
+    rng = np.random.default_rng(K + R)
+    words = lambda *s: rng.integers(0, 1 << 32, size=(*s, K // 8), dtype=np.uint32).view(np.int32)
+    a = words(R), np.full((R, ref.mx_scale_bytes(K)), a_byte, np.uint8)
+    w = words(E, N), np.full((E, N, ref.mx_scale_bytes(K)), w_byte, np.uint8)
+    off = np.linspace(0, R, E + 1).astype(np.int32)
+    want, size = ref.mx_product(ref.mx_values(*a), ref.mx_values(*w), off)
+    got = _host(ops.moe_mxfp4_grouped_gemm(*(_gpu(t) for t in (*a, *w, off)))).astype(np.float64)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= K * 2.0 ** -24 * size * (a_byte + w_byte > 127 + 24) + 2.0 ** -150).all()
