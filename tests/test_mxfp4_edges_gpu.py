@@ -1,4 +1,7 @@
-"""GPU: the MXFP4 and row calls where ordinary inputs do not lead."""
+"""GPU: the MXFP4 and row calls where ordinary inputs do not lead: sums near the ends
+of fp32, rows without a token, scales at the ends of their range, empty batches, and
+work that is still on its way on a side stream.
+"""
 
 from __future__ import annotations
 
@@ -210,3 +213,67 @@ def test_product_with_scale_bytes_0_and_254(ops, E, R, N, K, a_byte, w_byte):
     got = _host(ops.moe_mxfp4_grouped_gemm(*(_gpu(t) for t in (*a, *w, off)))).astype(np.float64)
     assert np.isfinite(got).all()
     assert (np.abs(got - want) <= K * 2.0 ** -24 * size * (a_byte + w_byte > 127 + 24) + 2.0 ** -150).all()
+
+
+# ---- streams ------------------------------------------------------------------------------
+def _stream_cases(ops):
+    """name: (inputs that arrive late, call).  Zeros are valid in the place of every input."""
+    rng = np.random.default_rng(31)
+    T, k, E, H, I = 40, 4, 16, 256, 96
+    S = T * k
+    randn = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).cuda()
+    ids = _gpu(np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32))
+    perm = ops.moe_permute_masked(ids, E)
+    xq = ops.moe_mxfp4_quantize(randn(S, H))
+    w = {}
+    for name, n, c in (("w13", 2 * I, H), ("w2", H, I)):
+        codes, scales = ops.moe_mxfp4_quantize(randn(E * n, c) / c ** 0.5)
+        w[name + "_codes"], w[name + "_scales"] = codes.view(E, n, -1), scales.view(E, n, -1)
+    w13 = w["w13_codes"], w["w13_scales"]
+    weights, rows = torch.rand(T, k, device="cuda"), perm["slot_rows"]
+    return {
+        "quantize": ([randn(S, H)], ops.moe_mxfp4_quantize),
+        "dequantize": (list(xq), ops.moe_mxfp4_dequantize),
+        "grouped_gemm": (list(xq), lambda c, s: ops.moe_mxfp4_grouped_gemm(c, s, *w13, perm["expert_offsets"])),
+        "gate_up": (list(xq), lambda c, s: ops.moe_mxfp4_gate_up(c, s, *w13, perm["expert_offsets"])),
+        "layer_few": ([randn(3, E), randn(3, H)], lambda g, x: ops.moe_mxfp4_layer_forward(g, x, k, w)),
+        "layer": ([randn(T, E), randn(T, H)], lambda g, x: ops.moe_mxfp4_layer_forward(g, x, k, w)),
+        "layer_many": ([randn(100, E), randn(100, H)], lambda g, x: ops.moe_mxfp4_layer_forward(g, x, k, w)),
+        "permute_masked": ([ids], lambda i: tuple(ops.moe_permute_masked(i, E).values())),
+        "dispatch": ([randn(T, H)], lambda x: ops.moe_dispatch(x, rows, k)),
+        "dispatch_backward": ([randn(S, H)], lambda g: ops.moe_dispatch_backward(g, rows, k)),
+        "combine_masked": ([randn(S, H)], lambda y: ops.moe_combine_masked(y, weights, rows)),
+        "combine_backward": ([randn(T, H), randn(S, H)], lambda g, y: ops.moe_combine_backward(g, y, weights, rows)),
+    }
+
+
+@pytest.mark.parametrize("name", ["quantize", "dequantize", "grouped_gemm", "gate_up", "layer_few", "layer", "layer_many",
+                                  "permute_masked", "dispatch", "dispatch_backward", "combine_masked", "combine_backward"])
+def test_calls_wait_for_their_stream(ops, name):
+    """Inputs that arrive on a side stream behind twenty large products: the call returns before
+    they are there and computes from them, not from what the buffers held."""
+    real, call = _stream_cases(ops)[name]
+    as_tuple = lambda r: r if isinstance(r, tuple) else (r,)
+    want = [t.clone() for t in as_tuple(call(*real))]
+    late = [torch.zeros_like(t) for t in real]
+    m = torch.randn(8192, 8192, device="cuda").to(torch.bfloat16)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        product = torch.empty_like(m)
+        torch.mm(m, m, out=product)
+        call(*late)  # the side stream's buffers are there from here on
+    torch.cuda.synchronize()
+    arrived = torch.cuda.Event()
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            torch.mm(m, m, out=product)
+        for buffer, value in zip(late, real):
+            buffer.copy_(value)
+        arrived.record()
+        got = as_tuple(call(*late))
+        early = not arrived.query()
+    s.synchronize()
+    for g, v in zip(got, want):
+        assert torch.equal(g, v)
+    assert early
