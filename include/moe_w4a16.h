@@ -614,10 +614,13 @@ size_t moe_mxfp4_layer_workspace_bytes(int64_t T, int32_t top_k, int32_t E,
 /*
  * moe_mxfp4_layer_forward - moe_layer_forward on MXFP4 experts, activations
  * quantised too: moe_route_permute, moe_mxfp4_quantize of x, moe_mxfp4_gate_up
- * over moe_permute's sorted_slots, moe_mxfp4_grouped_gemm into fp32 rows and
- * moe_combine_masked, in one call; out is what those calls produce up to the
- * order of the products' fp32 sums (up to 6 tokens two launches do all of it;
- * from 7 tokens on the kernels are the calls' own).
+ * over its sorted_slots, moe_mxfp4_grouped_gemm into fp32 rows and
+ * moe_combine_masked, in one call.  out is what those calls produce up to the
+ * order of the products' fp32 sums.  Up to 6 tokens, 64 slots, 1024 experts
+ * and H = 16384 two launches of the layer's own do all of it.  Otherwise the
+ * calls' kernels run, with two differences: each token is quantised once and
+ * stored straight to its rows in expert order, which gate/up then reads in
+ * order, and past 64 tokens the permutation is moe_permute_masked's.
  *
  *   logits      in   fp32 [T, E]
  *   x, out      in, out  dtype [T, H], dense; out may be x

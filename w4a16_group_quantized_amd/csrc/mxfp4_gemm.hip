@@ -35,7 +35,8 @@ namespace {
 // below, whose hundred workgroups leave half of the compute units idle).  Below
 // four windows the split costs: 20 experts, 2048 x 1280: 8.6 us (7.6 unsplit).
 // Gate/up in four shares is slower there (10.7) and 3 % faster for one long row.
-// Three windows in flight or five waves per SIMD are slower.
+// Three windows in flight or five waves per SIMD are slower.  (Weights in the
+// memory-side cache throughout.)
 constexpr int kTokens = 16;
 
 struct Window {
@@ -162,9 +163,12 @@ __global__ __launch_bounds__(GATE_UP ? 256 * SPLIT : 256) void mx_stream_kernel(
 //
 // 512 experts, 1280 x 2560: 217 us for 40960 rows (4.85 TB/s, bound by memory;
 // one workgroup per tile, without the running ring, 252), 29 us for 80 rows
-// (4.4 TB/s).  One expert, 8191 x 8192 x 8192: 285 to 300 us, 3.7 to 3.9
-// PFLOP/s, half of the cycles in matrix instructions at the clock it runs at;
-// bound by the loads of a chunk and its products overlapping in two stages only.
+// (4.4 TB/s).  One expert, 8191 x 8192 x 8192: 282 to 301 us, 3.7 to 3.9
+// PFLOP/s, 53 % of the cycles in matrix instructions at the clock it runs at.  Per
+// chunk of 256 values a compute unit moves 192 KB of fragments out of LDS and 68 KB
+// into it, about 2080 cycles at 128 bytes each, and its matrix instructions take
+// 2048; a chunk takes about 4000, so the two hardly overlap: all eight waves start
+// on fragment reads behind the chunk's one barrier.
 //
 // Tokens behind a segment and weight rows behind N leave what LDS holds, or
 // rows that follow: each result depends on its own row and token only, and
@@ -650,6 +654,8 @@ void launch_stream(const MxGemmArgs& a, bool split, hipStream_t stream) {
 
 }  // namespace
 
+// The rules go by the mean rows per expert; their figures are of rows shared out
+// evenly.  Few experts that hold most of the rows take the shape that the mean gives.
 void launch_mx_gemm(const MxGemmArgs& a, hipStream_t stream) {
   const int active = a.E < a.rows ? a.E : a.rows;  // experts that can hold a row
   const int mean = a.rows / active;

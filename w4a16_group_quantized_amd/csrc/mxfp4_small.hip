@@ -4,8 +4,10 @@
 // permutation, quantisation, gate/up, down, combine) are latency: 33.6 us at one
 // token of 512 experts, 10 chosen, hidden 2560, intermediate 640, for 26 MB of
 // weights; 17.4 us in these two (24 against 44 at two tokens, 41 against 60 at
-// four, 52 against 63 at five, 64 against 73 at six).  Here every workgroup does
-// the small steps for itself:
+// four, 52 against 63 at five, 64 against 73 at six).  Those are of four sets of
+// inputs in turn, whose weights stay in the memory-side cache up to two tokens; from
+// HBM one token takes 19.6 and two 26.2.  Here every workgroup does the small steps
+// for itself:
 //   gate/up  routes the tokens (one wave each) while its other waves quantise
 //            them into LDS, then takes 32 columns of I of one expert, as the
 //            streaming product does

@@ -49,7 +49,8 @@ __device__ __forceinline__ int64_t a_row(const MxGemmArgs& p, int r) {
 // The experts' rows cut into tiles of `size`, experts ascending; an expert's
 // last tile may be short.  The whole wave counts: lane l the tiles of experts
 // [l per, (l + 1) per), then a scan over the lanes.  Offsets are held inside
-// [0, rows], so damaged ones cannot lead out of the tensors.
+// [0, rows]: an entry outside does not lead out of the tensors.  That they
+// ascend is the caller's to keep.
 constexpr int kHeld = 8;  // experts per lane whose offsets stay in registers
 
 struct Tiles {
