@@ -233,6 +233,7 @@ def _encode(x, noise, signed):
     n = x.numel()
     b = _blocks(x)
     scale = b.abs().amax(1) / 1.875
+    scale = torch.where(scale < 2.0 ** -126, torch.zeros_like(scale), scale)
     inverse = torch.where(scale > 0, 1.0 / scale, torch.zeros_like(scale)).unsqueeze(1)
     place = (b.abs() * inverse) * (2.0 ** -112 if signed else 2.0 ** -96)
     code = (place.view(torch.int32).long() + _blocks(noise)) >> 20
