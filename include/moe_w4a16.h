@@ -730,6 +730,176 @@ int moe_combine_backward(const void* grad_out, int32_t grad_dtype,
                          void* grad_y, int64_t grad_y_stride,
                          float* grad_weights, void* stream);
 
+/* ------------------------------------------------------------------------- *
+ * Training the experts: products of rows grouped by expert in 16 bits with
+ * their gradients, the activation between them, the router's gradient, and
+ * the step that updates the weights.  Typed tensors and dtype codes as above;
+ * gradients are calls of their own.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * moe_grouped_gemm - rows times their expert's weights:
+ *   out[r, n] = sum_k a[r, k] * w[e, n, k]
+ *                               for expert_offsets[e] <= r < expert_offsets[e+1]
+ * moe_grouped_gemm_backward - the gradient of the rows:
+ *   grad_a[r, k] = sum_n grad[r, n] * w[e, n, k]
+ * moe_grouped_gemm_backward_weights - the gradient of the weights:
+ *   grad_w[e, n, k] = sum_r grad[r, n] * a[r, k]   over the rows r of expert e,
+ * zeros for an expert without rows; accumulate == 1 adds the sums to what
+ * grad_w holds.  Products are exact, summed in fp32 (with what grad_w holds,
+ * too), rounded once to out_dtype.  Rows outside [expert_offsets[0],
+ * expert_offsets[E]) are not read, and those of out and grad_a left as they
+ * were.  Which kernel runs, and with it the order of a sum, goes by the sizes:
+ * a repeated call gives identical bits, another number of rows may differ in
+ * the last ones.
+ *
+ *   a               in   dtype [rows, K], stride a_stride; dtype fp16 or bf16
+ *   grad            in   dtype [rows, N], stride grad_stride
+ *   expert_offsets  in   int32 [E + 1], ascending, or NULL with E == 1: every
+ *                        row belongs to the one expert
+ *   w               in   dtype [E, N, K], dense
+ *   out             out  out_dtype [rows, N], stride out_stride
+ *   grad_a          out  out_dtype [rows, K], stride grad_a_stride
+ *   grad_w          out  out_dtype [E, N, K], dense (accumulate: in and out)
+ *   workspace       scratch, device, >= moe_grouped_gemm_backward_weights_
+ *                   workspace_bytes(...) bytes (may be NULL when that is 0);
+ *                   contents on entry are ignored.  Two calls that overlap in
+ *                   time must not share it.
+ *
+ * Any N, K, strides and element-aligned addresses; where N, K, the strides and
+ * the addresses are multiples of 8 elements the calls are several times as
+ * fast.  An output must not overlap an input.  rows == 0 is valid;
+ * moe_grouped_gemm_backward_weights then still writes grad_w.
+ *
+ * Limits: fp32 operands are MOE_ERR_UNSUPPORTED; 1 <= E <= 4096; 1 <= N, K <=
+ * 65536; N * K < 2^30; rows <= 2^27 and (rows / 16 + min(E, rows)) *
+ * ceil(max(N, K) / 64) < 2^24.
+ */
+int moe_grouped_gemm(const void* a, int32_t dtype, int64_t rows,
+                     int64_t a_stride, const int32_t* expert_offsets, int32_t E,
+                     const void* w, int32_t N, int32_t K, void* out,
+                     int32_t out_dtype, int64_t out_stride, void* stream);
+int moe_grouped_gemm_backward(const void* grad, int32_t dtype, int64_t rows,
+                              int64_t grad_stride,
+                              const int32_t* expert_offsets, int32_t E,
+                              const void* w, int32_t N, int32_t K,
+                              void* grad_a, int32_t out_dtype,
+                              int64_t grad_a_stride, void* stream);
+size_t moe_grouped_gemm_backward_weights_workspace_bytes(int64_t rows,
+                                                         int32_t E, int32_t N,
+                                                         int32_t K);
+int moe_grouped_gemm_backward_weights(
+    const void* grad, int32_t dtype, int64_t rows, int64_t grad_stride,
+    const void* a, int64_t a_stride, const int32_t* expert_offsets, int32_t E,
+    int32_t N, int32_t K, void* grad_w, int32_t out_dtype, int32_t accumulate,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_silu_mul - the activation between an expert's two products:
+ *   act[r, i] = SiLU(h[r, i]) * h[r, I + i],   SiLU(v) = v s, s = 1 / (1 + e^-v)
+ * (the gate's columns first, as w13's rows).
+ * moe_silu_mul_backward - its gradient:
+ *   grad_h[r, i]     = grad_act[r, i] * up * s (1 + gate (1 - s))
+ *   grad_h[r, I + i] = grad_act[r, i] * gate * s
+ * In fp32, rounded once.  With expert_offsets, rows outside [expert_offsets[0],
+ * expert_offsets[E]) are not read and left as they were.  grad_h may be h
+ * itself (same address and stride); otherwise outputs must not overlap inputs.
+ *
+ *   h, grad_h       dtype [rows, 2I], strides h_stride, grad_h_stride
+ *   act, grad_act   dtype [rows, I], strides act_stride, grad_stride
+ *   expert_offsets  in  int32 [E + 1], or NULL: all rows (E is not read)
+ *
+ * Limits: 1 <= I <= 32768 (any I); rows < 2^31; rows * ceil(I / 8) < 2^32 - 256.
+ */
+int moe_silu_mul(const void* h, int32_t dtype, int64_t rows, int32_t I,
+                 int64_t h_stride, const int32_t* expert_offsets, int32_t E,
+                 void* act, int64_t act_stride, void* stream);
+int moe_silu_mul_backward(const void* grad_act, int64_t grad_stride,
+                          const void* h, int64_t h_stride, int32_t dtype,
+                          int64_t rows, int32_t I,
+                          const int32_t* expert_offsets, int32_t E,
+                          void* grad_h, int64_t grad_h_stride, void* stream);
+
+/*
+ * moe_route_backward - moe_route's gradient: with w = topk_weights and g =
+ * grad_weights (moe_combine_backward's),
+ *   grad_logits[t, id_j] = w[t, j] * (g[t, j] - sum_i w[t, i] g[t, i])
+ * and 0 for every expert that the token did not choose.  A choice outside
+ * [0, E) has no logit and is not written; its weight counts in the sum.  An
+ * expert chosen twice gets the sum of both.
+ *
+ *   topk_ids      in   int32 [T, top_k]
+ *   topk_weights  in   fp32 [T, top_k]
+ *   grad_weights  in   fp32 [T, top_k]
+ *   grad_logits   out  out_dtype [T, E]
+ *
+ * Limits: 1 <= E <= 4096; 1 <= top_k <= 64; T * top_k < 2^31.
+ */
+int moe_route_backward(const int32_t* topk_ids, const float* topk_weights,
+                       const float* grad_weights, int64_t T, int32_t E,
+                       int32_t top_k, void* grad_logits, int32_t out_dtype,
+                       void* stream);
+
+/*
+ * moe_adamw - one AdamW step over `count` tensors at once:
+ *   g = grad * grad_scale[0]
+ *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32; p is rounded once to its type (and once to copy's), and is updated
+ * from m and v before these are rounded to their states.
+ *
+ * States of 8 bits: elements in blocks of MOE_ADAMW_BLOCK (the last may be
+ * short), per block one fp32 scale = largest magnitude / 1.875.  A code's
+ * value is scale times a small float: m sign, 4 exponent bits (bias 15), 3
+ * mantissa bits; v, which is not negative, 5 exponent bits (bias 31) and 3; an
+ * exponent of 0 is subnormal.  Zero codes and scales are zero moments.  Codes
+ * are rounded up with the probability of the part cut off, by 20 bits of noise
+ * that are a function of the element's number and `seed`; pass another seed at
+ * every step (the step's number will do), and another one per call where one
+ * step takes several.  v > 0 is never rounded to 0.  A block whose largest
+ * magnitude is under 2.2e-38 becomes zeros; one that holds an infinity or a
+ * NaN does not stay finite.
+ *
+ *   tensors     in   HOST array of `count` descriptions, read during the call:
+ *     n                elements (0: skipped)
+ *     param            in, out  param_dtype [n]
+ *     grad             in       grad_dtype [n]
+ *     m, v             in, out  fp32 [n], or uint8 codes [n]
+ *     m_scales,        in, out  fp32 [ceil(n / MOE_ADAMW_BLOCK)] with 8 bits;
+ *     v_scales                  not read with 32
+ *     copy             out      copy_dtype [n], the new param once more (16-bit
+ *                               weights beside fp32 ones), or NULL
+ *   state_bits  8 or 32, of every tensor of the call
+ *   grad_scale  in   fp32 [1] on the device, or NULL: 1 (clipping and loss
+ *                    scales without a synchronisation)
+ *
+ * No two buffers of a call may overlap.  The scalars are the call's: a captured
+ * graph repeats its step number, rate and seed when it is replayed.
+ *
+ * MOE_ERR_INVALID_ARG for state_bits, betas outside [0, 1), negative or
+ * non-finite lr, eps or weight_decay, step < 1.  Limits: n <= 2^33.
+ */
+#define MOE_ADAMW_BLOCK 128
+typedef struct moe_adamw_tensor {
+  int64_t n;
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scales;
+  float* v_scales;
+  void* copy;
+  int32_t param_dtype;
+  int32_t grad_dtype;
+  int32_t copy_dtype;
+  int32_t reserved; /* 0 */
+} moe_adamw_tensor;
+int moe_adamw(const moe_adamw_tensor* tensors, int32_t count,
+              int32_t state_bits, double lr, double beta1, double beta2,
+              double eps, double weight_decay, int64_t step, uint32_t seed,
+              const float* grad_scale, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

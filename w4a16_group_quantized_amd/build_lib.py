@@ -18,7 +18,8 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["abi.hip", "plan.hip", "route.hip", "permute.hip", "route_permute.hip",
            "router_gate.hip", "ffn_decode.hip", "ffn_prefill.hip", "combine.hip",
            "abi_mxfp4.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip", "mxfp4_small.hip",
-           "permute_masked.hip", "dispatch.hip"]
+           "permute_masked.hip", "dispatch.hip", "abi_train.hip", "grouped_gemm.hip",
+           "train_rows.hip", "adamw.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

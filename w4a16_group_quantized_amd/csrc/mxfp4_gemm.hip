@@ -199,60 +199,6 @@ struct TileShape {
   static_assert(kWaves * kScratch <= kStage, "results turn inside one stage");
 };
 
-// Loads from memory straight to LDS, 16 or 4 bytes per lane: from the lane's
-// offset `at` to consecutive places from LDS address `lds` on.  Written out
-// because the compiler, which does not see which stage a read of LDS meets,
-// would wait for every load on its way before it; the waits are
-// wait_loads_and_barrier's.  There is no result register that could be reused
-// too early, and the LDS arrays' addresses are taken, so what the memory
-// barriers of the waits cover includes them.
-struct Descriptor {
-  dwords4 d;
-};
-
-__device__ __forceinline__ Descriptor descriptor(const void* base, uint32_t bytes) {
-  const uint64_t at = reinterpret_cast<uint64_t>(base);
-  Descriptor r;
-  r.d[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at));
-  r.d[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(at >> 32)) & 0xFFFFu;
-  r.d[2] = __builtin_amdgcn_readfirstlane(bytes);
-  r.d[3] = kRawBuffer;
-  return r;
-}
-
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
-      (__attribute__((address_space(3))) const void*)p));
-}
-
-__device__ __forceinline__ void load16_to_lds(const Descriptor& r, uint32_t lds, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
-               "v"(at), "s"(r.d)
-               : "m0");
-}
-__device__ __forceinline__ void load4_to_lds(const Descriptor& r, uint32_t lds, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds),
-               "v"(at), "s"(r.d)
-               : "m0");
-}
-
-template <int N>
-__device__ __forceinline__ void wait_loads_and_barrier() {
-  // all but the N newest loads done, LDS reads done, then the barrier; nothing
-  // that touches memory moves across
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
-__device__ __forceinline__ void wait_lds_and_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // LDS only
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 template <typename S, bool GATE_UP, typename TO>
 __global__ __launch_bounds__(64 * S::kWaves) void mx_tile_kernel(MxGemmArgs p, int n_tiles) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[S::STAGES * S::kStage];

@@ -1,0 +1,61 @@
+// Declarations of the training operators shared by their HIP translation units
+// and the ABI layer (internal; not part of the public ABI).
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+// The three products of rows grouped by expert, all C[i, j] = sum_q X[i, q] Y[j, q]
+// in fp32 over fp16 or bf16 operands:
+//   kOut      out[r, n]       rows of a       x W[e, n, :]      over k
+//   kRows     grad_a[r, k]    rows of grad    x W[e, :, k]      over n
+//   kWeights  grad_w[e, n, k] columns of grad x columns of a    over the expert's rows
+enum class Product { kOut, kRows, kWeights };
+
+struct GroupedArgs {
+  const uint16_t* x;  // a (kOut) or grad: [rows, ...], row stride x_ld
+  int64_t x_ld;
+  const uint16_t* y;  // W [E, N, K], or a [rows, K] with row stride y_ld (kWeights)
+  int64_t y_ld;
+  int dtype;          // of x and y: MOE_F16 or MOE_BF16
+  const int* offsets; // [E + 1], or null with E == 1
+  int rows, E, N, K;
+  void* out;
+  int out_dtype;
+  int64_t out_ld;     // kOut, kRows
+  int accumulate;     // kWeights: added to what out holds
+  float* partial;     // kWeights: workspace of grouped_workspace_bytes
+};
+size_t grouped_workspace_bytes(int64_t rows, int E, int N, int K);
+void launch_grouped(Product p, const GroupedArgs& a, hipStream_t stream);
+
+// act = SiLU(gate) * up of h = [gate | up], rows [offsets[0], offsets[E]) or all.
+struct ActArgs {
+  const void* grad;   // backward only
+  int64_t grad_ld;
+  const void* h;
+  int64_t h_ld;
+  int dtype;
+  int rows, I;
+  const int* offsets;
+  int E;
+  void* out;          // act, or the gradient of h
+  int64_t out_ld;
+};
+void launch_silu_mul(const ActArgs& a, bool backward, hipStream_t stream);
+
+void launch_route_backward(const int* ids, const float* weights, const float* grad, int T, int E,
+                           int top_k, void* out, int out_dtype, hipStream_t stream);
+
+struct AdamwScalars {
+  float beta1, rest1, beta2, rest2;  // rest = 1 - beta
+  float keep, size, root, eps;       // 1 - lr wd, lr / c1, 1 / sqrt(c2)
+  const float* grad_scale;           // device, or null: 1
+  uint32_t seed;
+};
+void launch_adamw(const moe_adamw_tensor* tensors, int count, int state_bits,
+                  const AdamwScalars& s, hipStream_t stream);
+constexpr int kAdamwBlock = MOE_ADAMW_BLOCK;
+
+}  // namespace moe

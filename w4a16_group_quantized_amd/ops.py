@@ -61,6 +61,14 @@ EXPORTED = (
     "moe_dispatch_backward",
     "moe_combine_masked",
     "moe_combine_backward",
+    "moe_grouped_gemm",
+    "moe_grouped_gemm_backward",
+    "moe_grouped_gemm_backward_weights_workspace_bytes",
+    "moe_grouped_gemm_backward_weights",
+    "moe_silu_mul",
+    "moe_silu_mul_backward",
+    "moe_route_backward",
+    "moe_adamw",
 )
 
 FFN_GEMV, FFN_MFMA = 0, 1
@@ -98,7 +106,24 @@ _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _SZ = ctypes.c_size_t
 
+_F64 = ctypes.c_double
+
 _SIGNATURES = {
+    "moe_grouped_gemm": (
+        ctypes.c_int, [_P, _I32, _I64, _I64, _P, _I32, _P, _I32, _I32, _P, _I32, _I64, _P]),
+    "moe_grouped_gemm_backward": (
+        ctypes.c_int, [_P, _I32, _I64, _I64, _P, _I32, _P, _I32, _I32, _P, _I32, _I64, _P]),
+    "moe_grouped_gemm_backward_weights_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32]),
+    "moe_grouped_gemm_backward_weights": (
+        ctypes.c_int,
+        [_P, _I32, _I64, _I64, _P, _I64, _P, _I32, _I32, _I32, _P, _I32, _I32, _P, _SZ, _P]),
+    "moe_silu_mul": (ctypes.c_int, [_P, _I32, _I64, _I32, _I64, _P, _I32, _P, _I64, _P]),
+    "moe_silu_mul_backward": (
+        ctypes.c_int, [_P, _I64, _P, _I64, _I32, _I64, _I32, _P, _I32, _P, _I64, _P]),
+    "moe_route_backward": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _I32, _P, _I32, _P]),
+    "moe_adamw": (
+        ctypes.c_int,
+        [_P, _I32, _I32, _F64, _F64, _F64, _F64, _F64, _I64, ctypes.c_uint32, _P, _P]),
     "moe_mxfp4_scale_bytes": (ctypes.c_int, [_I32]),
     "moe_mxfp4_quantize": (ctypes.c_int, [_P, _I32, _I64, _I32, _I64, _P, _P, _P]),
     "moe_mxfp4_dequantize": (ctypes.c_int, [_P, _P, _I64, _I32, _P, _I32, _I64, _P]),
@@ -998,3 +1023,234 @@ def moe_combine_backward(grad_out: torch.Tensor, y_sorted: torch.Tensor,
          py, y_code, sy, pw, _dense("slot_rows", slot_rows, torch.int32, T * k), T, k, H, rows, po, so,
          _dense("grad_weights", grad_weights, torch.float32, T, k))
     return out, grad_weights
+
+
+# --------------------------------------------------------------------------- #
+# training the experts: 16-bit products grouped by expert with their gradients,
+# the activation between them, the router's gradient, and the weights' update
+# --------------------------------------------------------------------------- #
+def _operand(name: str, t: torch.Tensor):
+    """_matrix of a product's operand: fp16 or bf16."""
+    if t.dtype is torch.float32:
+        raise ValueError(f"{name} is {t.dtype}: the products take float16 or bfloat16")
+    return _matrix(name, t)
+
+
+def _grouped_rows(fn, name, x, w, expert_offsets, dtype, out, forward):
+    """moe_grouped_gemm and its gradient of the rows: x [R, K or N] -> [R, N or K]."""
+    px, code, sx, rows, inner = _operand(name, x)
+    if w.dim() != 3:
+        raise ValueError(f"w has shape {tuple(w.shape)}, not [E, N, K]")
+    E, N, K = w.shape
+    want, cols = (K, N) if forward else (N, K)
+    if inner != want:
+        raise ValueError(f"{name} has {inner} columns, w [{E}, {N}, {K}] takes {want}")
+    pw = _dense("w", w, x.dtype, E, N, K)
+    po = None if expert_offsets is None else _dense("expert_offsets", expert_offsets, torch.int32, E + 1)
+    if out is None:
+        out, ptr, o_code, so = _made(x, rows, cols, dtype or x.dtype)
+    else:
+        ptr, o_code, so = _sized("out", out, rows, cols)
+        _apart("out", out, **{name: x, "w": w.view(E * N, K)})
+    _run(fn, _device_of(x, w, expert_offsets, out), px, code, rows, sx, po, E, pw, N, K, ptr, o_code, so)
+    return out
+
+
+def moe_grouped_gemm(a: torch.Tensor, w: torch.Tensor, expert_offsets: torch.Tensor | None = None,
+                     dtype: torch.dtype | None = None, out: torch.Tensor | None = None):
+    """Rows a [R, K] times their expert's weights w [E, N, K], both fp16 or bf16: out [R, N] of
+    `dtype` (default: a's).  Without expert_offsets (E == 1) every row belongs to the one expert.
+    Rows outside the experts' segments are left as they were (undefined when out is made here)."""
+    return _grouped_rows("moe_grouped_gemm", "a", a, w, expert_offsets, dtype, out, True)
+
+
+def moe_grouped_gemm_backward(grad: torch.Tensor, w: torch.Tensor,
+                              expert_offsets: torch.Tensor | None = None,
+                              dtype: torch.dtype | None = None, out: torch.Tensor | None = None):
+    """moe_grouped_gemm's gradient of the rows: grad [R, N] and w [E, N, K] -> grad_a [R, K]."""
+    return _grouped_rows("moe_grouped_gemm_backward", "grad", grad, w, expert_offsets, dtype, out, False)
+
+
+def grouped_gemm_backward_weights_workspace_bytes(rows: int, E: int, N: int, K: int) -> int:
+    return int(load_library().moe_grouped_gemm_backward_weights_workspace_bytes(rows, E, N, K))
+
+
+def moe_grouped_gemm_backward_weights(grad: torch.Tensor, a: torch.Tensor,
+                                      expert_offsets: torch.Tensor | None = None,
+                                      dtype: torch.dtype | None = None,
+                                      out: torch.Tensor | None = None, accumulate: bool = False,
+                                      workspace: torch.Tensor | None = None):
+    """moe_grouped_gemm's gradient of the weights: grad [R, N] and a [R, K] -> grad_w [E, N, K] of
+    `dtype` (default: a's), zeros for an expert without rows.  accumulate adds to the given out."""
+    pg, code, sg, rows, N = _operand("grad", grad)
+    pa, a_code, sa, rows_a, K = _operand("a", a)
+    if rows_a != rows or a_code != code:
+        raise ValueError(f"a is {a.dtype} of {rows_a} rows, grad {grad.dtype} of {rows}")
+    po, E = None, 1
+    if expert_offsets is not None:
+        E = expert_offsets.numel() - 1
+        po = _dense("expert_offsets", expert_offsets, torch.int32, E + 1)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs the tensor to add to: pass out")
+        dtype = dtype or a.dtype
+        if dtype not in _DTYPE:
+            raise ValueError(f"dtype {dtype} is not float32, float16 or bfloat16")
+        out = a.new_empty((E, N, K), dtype=dtype)
+    elif out.dtype not in _DTYPE:
+        raise ValueError(f"out is {out.dtype}, not float32, float16 or bfloat16")
+    else:
+        _dense("out", out, out.dtype, E, N, K)
+        _apart("out", out.view(E * N, K), grad=grad, a=a)
+    if workspace is None:
+        need = grouped_gemm_backward_weights_workspace_bytes(rows, E, N, K)
+        if need:
+            workspace = a.new_empty(need, dtype=torch.uint8)
+    _run("moe_grouped_gemm_backward_weights", _device_of(grad, a, expert_offsets, out, workspace), pg,
+         code, rows, sg, pa, sa, po, E, N, K, out.data_ptr(), _DTYPE[out.dtype], int(accumulate),
+         *_bytes("workspace", workspace))
+    return out
+
+
+def _segments(expert_offsets: torch.Tensor | None):
+    """(pointer, experts) of the segments that bound an elementwise call (None: all rows)."""
+    if expert_offsets is None:
+        return None, 0
+    n = expert_offsets.numel()
+    if n < 2:
+        raise ValueError(f"expert_offsets has {n} entries, not E + 1")
+    return _dense("expert_offsets", expert_offsets, torch.int32, n), n - 1
+
+
+def moe_silu_mul(h: torch.Tensor, expert_offsets: torch.Tensor | None = None,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """SiLU(gate) * up of h = [gate | up] [R, 2I]: [R, I].  With expert_offsets, rows outside the
+    experts' segments are left as they were (undefined when out is made here)."""
+    ph, code, sh, rows, cols = _matrix("h", h)
+    if cols % 2:
+        raise ValueError(f"h has {cols} columns, not two halves")
+    po, E = _segments(expert_offsets)
+    if out is None:
+        out, ptr, _, so = _made(h, rows, cols // 2, h.dtype)
+    else:
+        ptr, _, so = _sized("out", out, rows, cols // 2, code)
+        _apart("out", out, h=h)
+    _run("moe_silu_mul", _device_of(h, expert_offsets, out), ph, code, rows, cols // 2, sh, po, E, ptr, so)
+    return out
+
+
+def moe_silu_mul_backward(grad_act: torch.Tensor, h: torch.Tensor,
+                          expert_offsets: torch.Tensor | None = None,
+                          out: torch.Tensor | None = None) -> torch.Tensor:
+    """moe_silu_mul's gradient: grad_h [R, 2I] of h's type.  out may be h itself."""
+    ph, code, sh, rows, cols = _matrix("h", h)
+    if cols % 2:
+        raise ValueError(f"h has {cols} columns, not two halves")
+    pg, _, sg = _sized("grad_act", grad_act, rows, cols // 2, code)
+    po, E = _segments(expert_offsets)
+    if out is None:
+        out, ptr, _, so = _made(h, rows, cols, h.dtype)
+    else:
+        ptr, _, so = _sized("out", out, rows, cols, code)
+        _apart("out", out, grad_act=grad_act)
+        if ptr != ph or so != sh:
+            _apart("out", out, h=h)
+    _run("moe_silu_mul_backward", _device_of(grad_act, h, expert_offsets, out), pg, sg, ph, sh, code, rows,
+         cols // 2, po, E, ptr, so)
+    return out
+
+
+def moe_route_backward(topk_ids: torch.Tensor, topk_weights: torch.Tensor, grad_weights: torch.Tensor,
+                       E: int, dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None):
+    """moe_route's gradient: topk_ids, topk_weights and the weights' gradient [T, top_k] -> grad_logits
+    [T, E] of `dtype`.  In 16 bits it is an operand of the products, which give the gate
+    projection's own gradients (one expert)."""
+    pw, T, k = _weights(topk_weights)
+    pi = _dense("topk_ids", topk_ids, torch.int32, T, k)
+    pg = _dense("grad_weights", grad_weights, torch.float32, T, k)
+    if out is None:
+        out, ptr, code, _ = _made(topk_weights, T, E, dtype)
+    else:
+        code = _DTYPE.get(out.dtype, -1)
+        ptr = _dense("out", out, out.dtype if code >= 0 else torch.float32, T, E)
+    _run("moe_route_backward", _device_of(topk_ids, topk_weights, grad_weights, out), pi, pw, pg, T, E, k,
+         ptr, code)
+    return out
+
+
+ADAMW_BLOCK = 128  # elements that share a scale in 8-bit states
+
+
+def adamw_states(param: torch.Tensor, bits: int = 32):
+    """Zero states (m, v) of a tensor for moe_adamw: fp32 tensors of its shape, or with 8 bits pairs
+    (codes uint8 of its shape, scales fp32 [blocks])."""
+    if bits == 32:
+        return tuple(torch.zeros_like(param, dtype=torch.float32) for _ in range(2))
+    if bits != 8:
+        raise ValueError(f"states have 8 or 32 bits, not {bits}")
+    blocks = -(-param.numel() // ADAMW_BLOCK)
+    return tuple((torch.zeros_like(param, dtype=torch.uint8), param.new_zeros(blocks, dtype=torch.float32))
+                 for _ in range(2))
+
+
+def adamw_state_values(state: tuple, signed: bool) -> torch.Tensor:
+    """The fp32 values of an 8-bit state (codes, scales); signed for m, not for v."""
+    codes, scales = state
+    c = codes.reshape(-1).to(torch.int32)
+    value = ((c & 127 if signed else c) << 20).view(torch.float32) * (2.0 ** 112 if signed else 2.0 ** 96)
+    value = value * scales.repeat_interleave(ADAMW_BLOCK)[: c.numel()]
+    return (torch.where(c > 127, -value, value) if signed else value).view(codes.shape)
+
+
+def moe_adamw(params: list, grads: list, m: list, v: list, *, lr: float, beta1: float = 0.9,
+              beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01, step: int,
+              seed: int = 0, copies: list | None = None, grad_scale: torch.Tensor | None = None) -> None:
+    """One AdamW step, in place, over lists of tensors (adamw_states makes m and v; all of a call have
+    32 bits or all 8).  copies: 16-bit (or other) tensors, or None, that get the new parameters too.
+    seed (8 bits): another one at every step.  grad_scale: fp32 [1] on the device."""
+    count = len(params)
+    if len(grads) != count or len(m) != count or len(v) != count or (copies is not None
+                                                                     and len(copies) != count):
+        raise ValueError(f"{count} params, {len(grads)} grads, {len(m)} m, {len(v)} v, "
+                         f"{count if copies is None else len(copies)} copies")
+    if count == 0:
+        return
+    bits = 8 if isinstance(m[0], tuple) else 32
+    dev = params[0].get_device()
+    table = []
+
+    def flat(name, i, t, n, dtype):
+        if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{name}[{i}] must be contiguous {dtype} of {n} elements on {params[0].device}, "
+                             f"is {t.dtype} of shape {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    def typed(name, i, t, n):
+        code = _DTYPE.get(t.dtype)
+        if code is None:
+            raise ValueError(f"{name}[{i}] is {t.dtype}, not float32, float16 or bfloat16")
+        return flat(name, i, t, n, t.dtype), code
+
+    for i in range(count):
+        p, mi, vi = params[i], m[i], v[i]
+        n = p.numel()
+        pp, p_code = typed("params", i, p, n)
+        pg, g_code = typed("grads", i, grads[i], n)
+        pc, c_code = (0, 0) if copies is None or copies[i] is None else typed("copies", i, copies[i], n)
+        if (isinstance(mi, tuple), isinstance(vi, tuple)) != (bits == 8, bits == 8):
+            raise ValueError(f"m[{i}] and v[{i}] are not states of {bits} bits as m[0] is")
+        if bits == 32:
+            states = (flat("m", i, mi, n, torch.float32), flat("v", i, vi, n, torch.float32), 0, 0)
+        else:
+            blocks = (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
+            states = (flat("m", i, mi[0], n, torch.uint8), flat("v", i, vi[0], n, torch.uint8),
+                      flat("m scales", i, mi[1], blocks, torch.float32),
+                      flat("v scales", i, vi[1], blocks, torch.float32))
+        table += (n, pp, pg, *states, pc, p_code | g_code << 32, c_code)
+    scale = None if grad_scale is None else _dense("grad_scale", grad_scale, torch.float32, 1)
+    if scale is not None:
+        _device_of(params[0], grad_scale)
+    elif dev < 0:
+        _device_of(params[0])
+    _run("moe_adamw", dev, (ctypes.c_int64 * len(table))(*table), count, bits, lr, beta1, beta2, eps,
+         weight_decay, step, seed & 0xFFFFFFFF, scale)
