@@ -9,6 +9,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
@@ -19,14 +21,13 @@ SOURCES = ["abi.hip", "plan.hip", "route.hip", "permute.hip", "route_permute.hip
            "router_gate.hip", "ffn_decode.hip", "ffn_prefill.hip", "combine.hip",
            "abi_mxfp4.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip", "mxfp4_small.hip",
            "permute_masked.hip", "dispatch.hip", "abi_train.hip", "grouped_gemm.hip",
-           "train_rows.hip", "adamw.hip"]
+           "grouped_out.hip", "grouped_rows.hip", "grouped_weights.hip", "train_rows.hip", "adamw.hip"]
 ARCH = "gfx950"
 
 FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     f"--offload-arch={ARCH}",
     "-Wall",
     "-Wno-unused-function",
@@ -43,16 +44,27 @@ def hipcc() -> str:
     return os.path.join(rocm, "bin", "hipcc")
 
 
-def build(verbose: bool = False) -> str:
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc(), *FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", *srcs, "-o", tmp]
+def _compile(source: str, obj: str, verbose: bool) -> None:
+    cmd = [hipcc(), *FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-c", os.path.join(CSRC, source), "-o", obj]
+    _run(cmd, verbose)
+
+
+def _run(cmd: list, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"hipcc failed with exit code {res.returncode}")
+
+
+def build(verbose: bool = False) -> str:
+    tmp = LIB_PATH + ".tmp"
+    with tempfile.TemporaryDirectory() as objects:
+        jobs = [(s, os.path.join(objects, s + ".o"), verbose) for s in SOURCES]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda job: _compile(*job), jobs))
+        _run([hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *(obj for _, obj, _ in jobs), "-o", tmp], verbose)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 
