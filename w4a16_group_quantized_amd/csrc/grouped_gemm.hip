@@ -6,40 +6,10 @@
 // Products are exact, sums are fp32 in a fixed order, and a result is rounded
 // once, at its store.  The operand that runs along the output's columns is the
 // instruction's rows, so a lane ends with consecutive columns of one output row.
-#include "tiles.h"
-#include "train.h"
-#include "typed.h"
+#include "grouped_tile.h"
 
 namespace moe {
 namespace {
-
-template <typename T>
-struct Fragment;
-template <>
-struct Fragment<F16> {
-  typedef _Float16 type __attribute__((ext_vector_type(8)));
-};
-template <>
-struct Fragment<BF16> {
-  typedef __bf16 type __attribute__((ext_vector_type(8)));
-};
-
-__device__ __forceinline__ f32x4 mfma16(F16, dwords4 a, dwords4 b, f32x4 c) {
-  using V = Fragment<F16>::type;
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b),
-                                                c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 mfma16(BF16, dwords4 a, dwords4 b, f32x4 c) {
-  using V = Fragment<BF16>::type;
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V, a),
-                                                 __builtin_bit_cast(V, b), c, 0, 0, 0);
-}
-
-// Rows [r0, r1) of expert e, inside the tensors whatever the offsets hold.
-__device__ __forceinline__ void segment(const GroupedArgs& p, int e, int& r0, int& r1) {
-  r0 = p.offsets == nullptr ? 0 : min(max(p.offsets[e], 0), p.rows);
-  r1 = p.offsets == nullptr ? p.rows : min(max(p.offsets[e + 1], 0), p.rows);
-}
 
 // ------------------------------------------------------------- any alignment --
 // Sizes, strides and addresses that the tile kernels' 16-byte loads do not take:
@@ -143,17 +113,6 @@ __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedArgs p, int col
   }
 }
 
-// f(operand type, output type) for a product's dtype codes.
-template <typename F>
-void with_types(const GroupedArgs& a, F&& f) {
-  with_dtype(a.out_dtype, [&](auto to) {
-    if (a.dtype == MOE_F16)
-      f(F16{}, to);
-    else
-      f(BF16{}, to);
-  });
-}
-
 template <Product P>
 void launch_any(const GroupedArgs& a, hipStream_t stream) {
   const int cols = P == Product::kOut ? a.N : a.K;
@@ -172,11 +131,21 @@ void launch_any(const GroupedArgs& a, hipStream_t stream) {
 
 size_t grouped_workspace_bytes(int64_t, int, int, int) { return 0; }
 
+// What the tile kernels' 16-byte loads and 32-bit offsets take.
+static bool tiles_take(Product p, const GroupedArgs& a) {
+  auto whole = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };
+  constexpr int64_t kMaxLd = 1 << 20;
+  if (a.N % 8 || a.K % 8 || a.x_ld % 8 || a.x_ld > kMaxLd || !whole(a.x) || !whole(a.y)) return false;
+  return p != Product::kWeights || (a.y_ld % 8 == 0 && a.y_ld <= kMaxLd);
+}
+
 void launch_grouped(Product p, const GroupedArgs& a, hipStream_t stream) {
+  const bool tiles = tiles_take(p, a);
   switch (p) {
-    case Product::kOut: return launch_any<Product::kOut>(a, stream);
-    case Product::kRows: return launch_any<Product::kRows>(a, stream);
-    case Product::kWeights: return launch_any<Product::kWeights>(a, stream);
+    case Product::kOut: return tiles ? launch_grouped_out(a, stream) : launch_any<Product::kOut>(a, stream);
+    case Product::kRows: return tiles ? launch_grouped_rows(a, stream) : launch_any<Product::kRows>(a, stream);
+    case Product::kWeights:
+      return tiles ? launch_grouped_weights(a, stream) : launch_any<Product::kWeights>(a, stream);
   }
 }
 

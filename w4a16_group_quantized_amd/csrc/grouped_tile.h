@@ -1,0 +1,438 @@
+// The tile kernel of the grouped products (grouped_gemm.hip says what they are):
+// C[i, j] = sum_q X[i, q] Y[j, q], output rows i, output columns j.
+//
+// A workgroup takes tiles of BM rows x BN columns, one after the other, and walks
+// the reduction in chunks of 64, which go from memory straight to LDS in a ring of
+// STAGES; the sequence of chunks runs on over the tiles.  An operand whose
+// reduction is contiguous in memory is kept as rows of 128 bytes, their 16-byte
+// blocks numbered xor a few bits of the row's, so that the 16-byte reads of 16
+// rows meet all banks.  One whose reduction runs across the rows (W in the gradient
+// of the rows, both operands in that of the weights) is kept as it lies, 64 rows of
+// BM or BN values, and read through the transposing LDS load: 16 lanes fetch 4
+// reduction rows x 16 values, and each gets the 4 of its own column.  There the
+// blocks are numbered xor the row's two low bits, which sets the four rows of a
+// read into different quarters of the banks.
+//
+// Fragments are read one step (16 of the reduction) ahead of their products, across
+// the chunks too: the barrier that lets a chunk be replaced stands before the last
+// step's products, whose fragments are in registers by then, and behind it the next
+// chunk's first fragments are read.  A wave so has products to issue on both sides
+// of the one barrier of a chunk.
+#pragma once
+
+#include "tiles.h"
+#include "train.h"
+#include "typed.h"
+
+namespace moe {
+
+template <typename T>
+struct Fragment;
+template <>
+struct Fragment<F16> {
+  typedef _Float16 type __attribute__((ext_vector_type(8)));
+};
+template <>
+struct Fragment<BF16> {
+  typedef __bf16 type __attribute__((ext_vector_type(8)));
+};
+
+__device__ __forceinline__ f32x4 mfma16(F16, dwords4 a, dwords4 b, f32x4 c) {
+  using V = Fragment<F16>::type;
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b),
+                                                c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma16(BF16, dwords4 a, dwords4 b, f32x4 c) {
+  using V = Fragment<BF16>::type;
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V, a),
+                                                 __builtin_bit_cast(V, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(F16, dwords4 a, dwords4 b, f32x16 c) {
+  using V = Fragment<F16>::type;
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b),
+                                                c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(BF16, dwords4 a, dwords4 b, f32x16 c) {
+  using V = Fragment<BF16>::type;
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(V, a),
+                                                 __builtin_bit_cast(V, b), c, 0, 0, 0);
+}
+
+// Rows [r0, r1) of expert e, inside the tensors whatever the offsets hold.
+__device__ __forceinline__ void segment(const GroupedArgs& p, int e, int& r0, int& r1) {
+  r0 = p.offsets == nullptr ? 0 : min(max(p.offsets[e], 0), p.rows);
+  r1 = p.offsets == nullptr ? p.rows : min(max(p.offsets[e + 1], 0), p.rows);
+}
+
+constexpr int kChunk = 64;      // of the reduction
+constexpr int kChunkRow = 128;  // bytes of it in a row
+
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
+struct GroupedShape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
+  static constexpr int kWaves = WM * WN;
+  static constexpr int MT = BM / 32 / WM, NT = BN / 32 / WN;  // 32 x 32 results per wave
+  static constexpr int kX = BM * kChunkRow, kY = BN * kChunkRow, kStage = kX + kY;
+  static constexpr int kLoadX = kX / 1024 / kWaves, kLoadY = kY / 1024 / kWaves;
+  static constexpr int kLoads = kLoadX + kLoadY;              // per wave and chunk
+  static constexpr int kTurn = 128, kScratch = 32 * kTurn;    // results turn per wave, below
+  static constexpr int kLds = STAGES * kStage + static_cast<int>(sizeof(TileTable));
+  static constexpr int kPerCu = static_cast<int>(kGfx950LdsBytes) / kLds;
+  static_assert(kPerCu >= 1, "the ring fits in LDS");
+  static_assert(kLoadX * kWaves * 1024 == kX && kLoadY * kWaves * 1024 == kY, "loads divide evenly");
+  static_assert(kWaves * kScratch <= kStage, "results turn inside one stage");
+};
+
+// One operand's way through memory: where the next chunk begins and how many bytes
+// there are from there (all uniform), and this lane's offset in a chunk.
+template <int B, int WAVES, bool ALONG>
+struct Stream {
+  static constexpr int kLoad = B * kChunkRow / 1024 / WAVES;
+  const uint8_t* at;
+  int64_t left, step;
+  uint32_t lane_at, load_step;
+  int depth_at;  // ALONG: where in the chunk this lane's values lie
+
+  static __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
+    return ALONG ? (row >> 1) & 7 : (row & 3) << 2;
+  }
+  __device__ __forceinline__ void init(int wave, int64_t ld) {
+    const uint32_t u = wave * 64 + (threadIdx.x & 63);
+    constexpr uint32_t kBlocks = ALONG ? 8 : B / 8;  // of 16 bytes per row in LDS
+    static_assert(ALONG || kBlocks >= 16, "the swizzle stays inside a row");
+    const uint32_t row = u / kBlocks, blk = (u % kBlocks) ^ swizzle(row);
+    lane_at = row * static_cast<uint32_t>(ld * 2) + blk * 16;
+    load_step = WAVES * 64 / kBlocks * static_cast<uint32_t>(ld * 2);
+    depth_at = ALONG ? blk * 8 : 0;
+    step = ALONG ? kChunkRow : kChunk * ld * 2;
+  }
+  // Requests the chunk into LDS from address `lds` on; `depth` values of the reduction
+  // are left.  Blocks behind it, and rows behind the tensor, become zeros.
+  __device__ __forceinline__ void load(uint32_t lds, int wave, int depth) {
+    const int64_t n = left < 0 ? 0 : left;
+    const Descriptor r = descriptor(at, static_cast<uint32_t>(n < INT32_MAX ? n : INT32_MAX));
+    uint32_t from = lane_at;
+    if (ALONG && depth < kChunk) from = depth_at < depth ? from : kOutOfRange;
+#pragma unroll
+    for (int i = 0; i < kLoad; ++i) {
+      load16_to_lds(r, lds + (i * WAVES + wave) * 1024, from);
+      from += load_step;
+    }
+    at += step;
+    left -= step;
+  }
+};
+
+// What a lane reads of an operand: fragment i, step s of the chunk at `st`.
+template <int B, bool ALONG>
+struct Reader {
+  uint32_t base;
+  __device__ __forceinline__ void init(int first) {  // the wave's first row or column
+    const uint32_t lane = threadIdx.x & 63;
+    if constexpr (ALONG) {
+      const uint32_t row = first + (lane & 31);
+      base = row * kChunkRow + ((lane >> 5) ^ ((row >> 1) & 7)) * 16;
+    } else {
+      const uint32_t l = lane & 15, q = (lane >> 5) * 8 + (l >> 2);  // q & 3 == l >> 2
+      const uint32_t c = first + ((lane >> 4) & 1) * 16 + (l & 3) * 4;
+      base = q * (B * 2) + (((c >> 3) ^ ((l >> 2) << 2)) * 16) + (c & 4) * 2;
+    }
+  }
+  __device__ __forceinline__ dwords4 read(const uint8_t* st, int i, int s) const {
+    if constexpr (ALONG) {
+      return *reinterpret_cast<const dwords4*>(st + (base ^ (32 * s)) + i * 32 * kChunkRow);
+    } else {
+      typedef short v4i16 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) v4i16* LdsPtr;
+      const uint8_t* p = st + (base ^ (i * 64)) + s * 16 * B * 2;
+      const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p));
+      const auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p + 4 * B * 2));
+      const dwords2 a = __builtin_bit_cast(dwords2, lo), b = __builtin_bit_cast(dwords2, hi);
+      return dwords4{a[0], a[1], b[0], b[1]};
+    }
+  }
+};
+
+template <typename S, Product P, typename T, typename TO>
+__global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArgs p, int col_tiles) {
+  __shared__ __attribute__((aligned(16))) uint8_t ring[S::STAGES * S::kStage];
+  __shared__ TileTable table;
+  constexpr bool kAlongX = P != Product::kWeights, kAlongY = P == Product::kOut;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int cols = P == Product::kOut ? p.N : p.K;
+
+  // Tiles in groups of kGroupTiles row tiles, rows fastest, and each XCD (the
+  // workgroups of equal index mod 8) a contiguous run of them: the tiles that run
+  // together share both operands in its L2.
+  constexpr int kGroupTiles = 4;
+  const int w_tiles = (p.N + S::BM - 1) / S::BM;  // kWeights: row tiles of an expert
+  const int total = P == Product::kWeights
+                        ? p.E * w_tiles
+                        : keep_tiles(count_tiles(p.offsets, p.E, p.rows, S::BM), table);
+  const int all = total * col_tiles;
+  const int run = (all + 7) >> 3;
+  const int run0 = (blockIdx.x & 7) * run;
+  const int run_n = min(run, all - run0);
+  const int first_tile = blockIdx.x >> 3, step = gridDim.x >> 3;
+  if (first_tile >= run_n) return;
+  const int mine = (run_n - first_tile + step - 1) / step;
+  struct Tile {
+    int e, i0, i1, j0;  // rows [i0, i1) and columns from j0 on of the output
+    int r0, depth;      // kWeights: first row of the segment; terms of the sums
+  };
+  auto locate = [&](int j) {
+    const int tile = run0 + first_tile + j * step;
+    Tile t;
+    if constexpr (P == Product::kWeights) {
+      const int per = w_tiles * col_tiles;
+      t.e = tile / per;
+      const int at = tile - t.e * per;
+      const int grp = at / (kGroupTiles * col_tiles);
+      const int in = at - grp * kGroupTiles * col_tiles;
+      const int gm = min(kGroupTiles, w_tiles - grp * kGroupTiles);
+      const int nt = in / gm;
+      t.i0 = (grp * kGroupTiles + in - nt * gm) * S::BM;
+      t.i1 = min(p.N, t.i0 + S::BM);
+      t.j0 = nt * S::BN;
+      int r1;
+      segment(p, t.e, t.r0, r1);
+      t.depth = max(r1 - t.r0, 0);
+    } else {
+      const int grp = tile / (kGroupTiles * col_tiles);
+      const int in = tile - grp * kGroupTiles * col_tiles;
+      const int gm = min(kGroupTiles, total - grp * kGroupTiles);
+      const int nt = in / gm;
+      t.j0 = nt * S::BN;
+      find_tile(kept_tiles(table, p.offsets, p.E, p.rows, S::BM, total),
+                grp * kGroupTiles + in - nt * gm, t.e, t.i0, t.i1);
+      t.r0 = 0;
+      t.depth = P == Product::kOut ? p.K : p.N;
+    }
+    return t;
+  };
+  // an expert without rows still has a chunk (of zeros)
+  auto chunks_of = [](const Tile& t) { return max(1, (t.depth + kChunk - 1) / kChunk); };
+
+  // ---- loads: the tile and chunk that are requested next
+  Stream<S::BM, S::kWaves, kAlongX> sx;
+  Stream<S::BN, S::kWaves, kAlongY> sy;
+  sx.init(wave, p.x_ld);
+  sy.init(wave, P == Product::kWeights ? p.y_ld : p.K);
+  int load_left = 0;  // of the reduction
+  auto aim = [&](const Tile& t) {
+    load_left = t.depth;
+    if constexpr (P == Product::kWeights) {
+      // rows of the segment, each from the tile's first column to the matrix's last
+      const int64_t n = t.depth;
+      sx.at = reinterpret_cast<const uint8_t*>(p.x + t.r0 * p.x_ld + t.i0);
+      sx.left = n > 0 ? ((n - 1) * p.x_ld + p.N - t.i0) * 2 : 0;
+      sy.at = reinterpret_cast<const uint8_t*>(p.y + t.r0 * p.y_ld + t.j0);
+      sy.left = n > 0 ? ((n - 1) * p.y_ld + p.K - t.j0) * 2 : 0;
+    } else {
+      sx.at = reinterpret_cast<const uint8_t*>(p.x + t.i0 * p.x_ld);
+      sx.left = (static_cast<int64_t>(t.i1 - t.i0 - 1) * p.x_ld + t.depth) * 2;
+      const int64_t w = static_cast<int64_t>(p.N) * p.K;
+      const int64_t skip = P == Product::kOut ? static_cast<int64_t>(t.j0) * p.K : t.j0;
+      sy.at = reinterpret_cast<const uint8_t*>(p.y + t.e * w + skip);
+      sy.left = (w - skip) * 2;
+    }
+  };
+  int load_tile = 0;
+  const uint32_t ring_at = lds_address(ring);
+  uint32_t load_at = ring_at;
+  // Requests the next chunk and moves on, to the next tile behind a tile's last.
+  // Behind the last tile the loads have empty ranges (nothing is fetched), so that
+  // the number on their way is always the same.
+  auto load_next = [&]() {
+    sx.load(load_at, wave, load_left);
+    sy.load(load_at + S::kX, wave, load_left);
+    load_left -= kChunk;
+    load_at = load_at == ring_at + (S::STAGES - 1) * S::kStage ? ring_at : load_at + S::kStage;
+    if (load_left <= 0) {
+      if (++load_tile < mine) {
+        aim(locate(load_tile));
+      } else {
+        sx.left = sy.left = 0;
+        load_left = INT32_MAX;
+      }
+    }
+  };
+
+  // ---- products
+  const int col = lane & 31, g = lane >> 5;
+  Reader<S::BM, kAlongX> rx;
+  Reader<S::BN, kAlongY> ry;
+  rx.init(wm * S::MT * 32);
+  ry.init(wn * S::NT * 32);
+  f32x16 acc[S::NT][S::MT];
+  struct Step {
+    dwords4 x[S::MT], y[S::NT];
+  };
+  auto read = [&](const uint8_t* st, int s) {
+    Step f;
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j) f.y[j] = ry.read(st + S::kX, j, s);
+#pragma unroll
+    for (int i = 0; i < S::MT; ++i) f.x[i] = rx.read(st, i, s);
+    return f;
+  };
+  auto multiply = [&](const Step& f) {
+#pragma unroll
+    for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) acc[j][i] = mfma32(T{}, f.y[j], f.x[i], acc[j][i]);
+  };
+  // Zeros, or what the output holds.
+  auto begin = [&](const Tile& t) {
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+      for (int i = 0; i < S::MT; ++i) acc[j][i] = f32x16{};
+    if constexpr (P == Product::kWeights) {
+      if (!p.accumulate || t.depth == 0) return;
+#pragma unroll
+      for (int i = 0; i < S::MT; ++i) {
+        const int row = t.i0 + (wm * S::MT + i) * 32 + col;
+        const auto* o = static_cast<const typename TO::bits*>(p.out) +
+                        (static_cast<int64_t>(t.e) * p.N + min(row, p.N - 1)) * p.K;
+#pragma unroll
+        for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int c = t.j0 + (wn * S::NT + j) * 32 + 8 * (r / 4) + 4 * g + r % 4;
+            if (c < p.K) acc[j][i][r] = to_float(TO{}, o[c]);
+          }
+      }
+    }
+  };
+
+  // acc[j][i][4 q + r] is column 32 j' + 8 q + 4 g + r of row 32 i' + col.  Results
+  // turn in LDS, 32 rows x kTurn bytes of them at a time, so that eight neighbouring
+  // lanes store that many contiguous bytes of a row.  `turn` is this wave's place; a
+  // row's 16-byte slots are stored with their number xor a few bits of the row's.
+  auto store = [&](const Tile& t, uint8_t* turn) {
+    if (P == Product::kWeights && p.accumulate && t.depth == 0) return;
+    constexpr int kCols = S::kTurn / kBytes<TO>, kSlots = S::kTurn / 16, kRows = 64 / kSlots;
+    static_assert(S::NT * 32 % kCols == 0 || kCols % (S::NT * 32) == 0, "columns turn evenly");
+    constexpr int kWide = kCols < S::NT * 32 ? kCols : S::NT * 32;
+    auto slot = [](int row, int n) { return (n ^ row) & (kSlots - 1); };
+    const int64_t out_ld = P == Product::kWeights ? p.K : p.out_ld;
+    auto* out = static_cast<typename TO::bits*>(p.out) +
+                (P == Product::kWeights ? static_cast<int64_t>(t.e) * p.N * p.K : 0);
+#pragma unroll
+    for (int i = 0; i < S::MT; ++i) {
+      const int row0 = t.i0 + (wm * S::MT + i) * 32;
+      if (row0 >= t.i1) break;
+#pragma unroll
+      for (int c0 = 0; c0 < S::NT * 32; c0 += kWide) {
+#pragma unroll
+        for (int c = 0; c < kWide; c += 8) {  // columns c0 + c + 4 g ... + 3
+          f32x4 v;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = acc[(c0 + c) / 32][i][(c0 + c) % 32 / 2 + r];
+          const int at = (c + 4 * g) * kBytes<TO>;
+          uint8_t* to = turn + col * S::kTurn + slot(col, at >> 4) * 16;
+          if constexpr (kBytes<TO> == 4)
+            *reinterpret_cast<dwords4*>(to) = __builtin_bit_cast(dwords4, v);
+          else
+            *reinterpret_cast<dwords2*>(to + (at & 8)) = pack4<TO>(v);
+        }
+        const int in = lane % kSlots * (16 / kBytes<TO>);
+        const int j = t.j0 + wn * S::NT * 32 + c0 + in;
+#pragma unroll
+        for (int r = 0; r < 32; r += kRows) {
+          const int row = r + lane / kSlots;
+          const dwords4 d =
+              *reinterpret_cast<const dwords4*>(turn + row * S::kTurn + slot(row, lane) * 16);
+          if (row0 + row >= t.i1 || (kWide < kCols && in >= kWide)) continue;
+          auto* o = out + (row0 + row) * out_ld + j;
+          if (j + 16 / kBytes<TO> <= cols) {
+            store16(o, d);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 16 / kBytes<TO>; ++x)
+              if (j + x < cols)
+                o[x] = static_cast<typename TO::bits>(
+                    kBytes<TO> == 4 ? d[x % 4] : d[x / 2] >> (16 * (x & 1)));
+          }
+        }
+      }
+    }
+  };
+
+  aim(locate(0));
+#pragma unroll
+  for (int s = 0; s < S::STAGES; ++s) load_next();
+  wait_loads_and_barrier<(S::STAGES - 1) * S::kLoads>();
+  uint32_t stage = 0;
+  Tile t = locate(0);
+  int chunks = chunks_of(t);
+  begin(t);
+  Step f = read(ring, 0);
+  for (int n = 0, c = 0;;) {
+    const uint8_t* st = ring + stage;
+    Step f1 = read(st, 1);
+    multiply(f);
+    f = read(st, 2);
+    multiply(f1);
+    f1 = read(st, 3);
+    multiply(f);
+    // every wave holds its last fragments of this chunk; the next one is there when
+    // only those behind it are on their way (stores among them make the wait
+    // longer, never too short)
+    wait_loads_and_barrier<(S::STAGES - 2) * S::kLoads>();
+    const uint32_t free = stage;
+    stage = stage + S::kStage == S::STAGES * S::kStage ? 0 : stage + S::kStage;
+    const bool last = ++c == chunks;
+    if (!last) load_next();
+    f = read(ring + stage, 0);
+    multiply(f1);
+    if (!last) continue;
+    // results leave through the place that is free now, which is loaded after that
+    store(t, ring + free + wave * S::kScratch);
+    wait_lds_and_barrier();
+    load_next();
+    if (++n == mine) break;
+    t = locate(n);
+    chunks = chunks_of(t);
+    c = 0;
+    begin(t);
+  }
+  // no load into this workgroup's LDS outlives it
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+}
+
+// f(operand type, output type) for a product's dtype codes.
+template <typename F>
+void with_types(const GroupedArgs& a, F&& f) {
+  with_dtype(a.out_dtype, [&](auto to) {
+    if (a.dtype == MOE_F16)
+      f(F16{}, to);
+    else
+      f(BF16{}, to);
+  });
+}
+
+template <typename S, Product P>
+void launch_grouped_tiles(const GroupedArgs& a, hipStream_t stream) {
+  const int cols = P == Product::kOut ? a.N : a.K;
+  const int col_tiles = (cols + S::BN - 1) / S::BN;
+  // at most one short tile per expert; no more workgroups than run at once
+  const int64_t row_tiles =
+      P == Product::kWeights ? static_cast<int64_t>(a.E) * ((a.N + S::BM - 1) / S::BM)
+                             : a.rows / S::BM + (a.E < a.rows ? a.E : a.rows);
+  const int64_t resident = static_cast<int64_t>(device_info().cus) * S::kPerCu;
+  const int64_t groups = row_tiles * col_tiles < resident ? row_tiles * col_tiles : resident;
+  const dim3 grid(static_cast<unsigned>((groups + 7) / 8 * 8)), block(64 * S::kWaves);
+  with_types(a, [&](auto t, auto to) {
+    hipLaunchKernelGGL((grouped_tile_kernel<S, P, decltype(t), decltype(to)>), grid, block, 0,
+                       stream, a, col_tiles);
+  });
+}
+
+using Grouped256 = GroupedShape<256, 256, 2, 4, 2>;
+using Grouped128 = GroupedShape<128, 128, 2, 2, 2>;
+
+}  // namespace moe

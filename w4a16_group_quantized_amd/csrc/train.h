@@ -28,6 +28,10 @@ struct GroupedArgs {
   float* partial;     // kWeights: workspace of grouped_workspace_bytes
 };
 size_t grouped_workspace_bytes(int64_t rows, int E, int N, int K);
+// With tiles of 16-byte loads (grouped_out.hip, grouped_rows.hip, grouped_weights.hip).
+void launch_grouped_out(const GroupedArgs& a, hipStream_t stream);
+void launch_grouped_rows(const GroupedArgs& a, hipStream_t stream);
+void launch_grouped_weights(const GroupedArgs& a, hipStream_t stream);
 void launch_grouped(Product p, const GroupedArgs& a, hipStream_t stream);
 
 // act = SiLU(gate) * up of h = [gate | up], rows [offsets[0], offsets[E]) or all.
