@@ -13,16 +13,18 @@
 // blocks are numbered xor the row's two low bits, which sets the four rows of a
 // read into different quarters of the banks.
 //
-// Fragments are read one step (16 of the reduction) ahead of their products, across
-// the chunks too: the barrier that lets a chunk be replaced stands before the last
-// step's products, whose fragments are in registers by then, and behind it the next
-// chunk's first fragments are read.  A wave so has products to issue on both sides
-// of the one barrier of a chunk.
+// Fragments are read half a step (a step is 32 of the reduction; half of the wave's
+// rows) ahead of their products, across the chunks too: the barrier that lets a chunk
+// be replaced stands before the last half step's products, whose fragments are in
+// registers by then, and behind it the next chunk's first fragments are read.  A wave
+// so has products to issue on both sides of the one barrier of a chunk.
 #pragma once
 
 #include "tiles.h"
 #include "train.h"
 #include "typed.h"
+
+#include <type_traits>
 
 namespace moe {
 
@@ -47,17 +49,6 @@ __device__ __forceinline__ f32x4 mfma16(BF16, dwords4 a, dwords4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V, a),
                                                  __builtin_bit_cast(V, b), c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x16 mfma32(F16, dwords4 a, dwords4 b, f32x16 c) {
-  using V = Fragment<F16>::type;
-  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(V, a), __builtin_bit_cast(V, b),
-                                                c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x16 mfma32(BF16, dwords4 a, dwords4 b, f32x16 c) {
-  using V = Fragment<BF16>::type;
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(V, a),
-                                                 __builtin_bit_cast(V, b), c, 0, 0, 0);
-}
-
 // Rows [r0, r1) of expert e, inside the tensors whatever the offsets hold.
 __device__ __forceinline__ void segment(const GroupedArgs& p, int e, int& r0, int& r1) {
   r0 = p.offsets == nullptr ? 0 : min(max(p.offsets[e], 0), p.rows);
@@ -71,16 +62,16 @@ template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
 struct GroupedShape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
   static constexpr int kWaves = WM * WN;
-  static constexpr int MT = BM / 32 / WM, NT = BN / 32 / WN;  // 32 x 32 results per wave
+  static constexpr int MT = BM / 16 / WM, NT = BN / 16 / WN;  // 16 x 16 results per wave
   static constexpr int kX = BM * kChunkRow, kY = BN * kChunkRow, kStage = kX + kY;
   static constexpr int kLoadX = kX / 1024 / kWaves, kLoadY = kY / 1024 / kWaves;
   static constexpr int kLoads = kLoadX + kLoadY;              // per wave and chunk
-  static constexpr int kTurn = 128, kScratch = 32 * kTurn;    // results turn per wave, below
-  static constexpr int kLds = STAGES * kStage + static_cast<int>(sizeof(TileTable));
+  static constexpr int kTurn = 128, kScratch = 16 * kTurn;    // results turn per wave, below
+  static constexpr int kLds = STAGES * kStage + kWaves * kScratch + static_cast<int>(sizeof(TileTable));
   static constexpr int kPerCu = static_cast<int>(kGfx950LdsBytes) / kLds;
   static_assert(kPerCu >= 1, "the ring fits in LDS");
   static_assert(kLoadX * kWaves * 1024 == kX && kLoadY * kWaves * 1024 == kY, "loads divide evenly");
-  static_assert(kWaves * kScratch <= kStage, "results turn inside one stage");
+  static_assert(kLoads % 2 == 0 && MT % 2 == 0, "chunks are requested and rows multiplied in halves");
 };
 
 // One operand's way through memory: where the next chunk begins and how many bytes
@@ -94,7 +85,7 @@ struct Stream {
   int depth_at;  // ALONG: where in the chunk this lane's values lie
 
   static __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
-    return ALONG ? (row >> 1) & 7 : (row & 3) << 2;
+    return ALONG ? (row >> 1) & 7 : ((row & 3) << 2) | ((row >> 2) & 2);
   }
   __device__ __forceinline__ void init(int wave, int64_t ld) {
     const uint32_t u = wave * 64 + (threadIdx.x & 63);
@@ -106,45 +97,47 @@ struct Stream {
     depth_at = ALONG ? blk * 8 : 0;
     step = ALONG ? kChunkRow : kChunk * ld * 2;
   }
-  // Requests the chunk into LDS from address `lds` on; `depth` values of the reduction
-  // are left.  Blocks behind it, and rows behind the tensor, become zeros.
-  __device__ __forceinline__ void load(uint32_t lds, int wave, int depth) {
+  // The chunk that is requested next; `depth` values of the reduction are left.  Blocks
+  // behind it, and rows behind the tensor, become zeros.
+  Descriptor range;
+  uint32_t from;
+  __device__ __forceinline__ void prepare(int depth) {
     const int64_t n = left < 0 ? 0 : left;
-    const Descriptor r = descriptor(at, static_cast<uint32_t>(n < INT32_MAX ? n : INT32_MAX));
-    uint32_t from = lane_at;
+    range = descriptor(at, static_cast<uint32_t>(n < INT32_MAX ? n : INT32_MAX));
+    from = lane_at;
     if (ALONG && depth < kChunk) from = depth_at < depth ? from : kOutOfRange;
-#pragma unroll
-    for (int i = 0; i < kLoad; ++i) {
-      load16_to_lds(r, lds + (i * WAVES + wave) * 1024, from);
-      from += load_step;
-    }
     at += step;
     left -= step;
   }
+  // Part i of it, into LDS from address `lds` on.
+  __device__ __forceinline__ void load(uint32_t lds, int wave, int i) const {
+    load16_to_lds(range, lds + (i * WAVES + wave) * 1024, from + i * load_step);
+  }
 };
 
-// What a lane reads of an operand: fragment i, step s of the chunk at `st`.
+// What a lane reads of an operand: fragment i (16 rows or columns), step s (32 of the
+// reduction) of the chunk at `st`.
 template <int B, bool ALONG>
 struct Reader {
   uint32_t base;
   __device__ __forceinline__ void init(int first) {  // the wave's first row or column
-    const uint32_t lane = threadIdx.x & 63;
+    const uint32_t l = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
     if constexpr (ALONG) {
-      const uint32_t row = first + (lane & 31);
-      base = row * kChunkRow + ((lane >> 5) ^ ((row >> 1) & 7)) * 16;
+      const uint32_t row = first + l;
+      base = row * kChunkRow + (g ^ ((row >> 1) & 7)) * 16;
     } else {
-      const uint32_t l = lane & 15, q = (lane >> 5) * 8 + (l >> 2);  // q & 3 == l >> 2
-      const uint32_t c = first + ((lane >> 4) & 1) * 16 + (l & 3) * 4;
-      base = q * (B * 2) + (((c >> 3) ^ ((l >> 2) << 2)) * 16) + (c & 4) * 2;
+      const uint32_t q = g * 8 + (l >> 2), c = first + (l & 3) * 4;
+      const uint32_t blk = (c >> 3) ^ Stream<B, 1, false>::swizzle(q);
+      base = q * (B * 2) + blk * 16 + (c & 4) * 2;
     }
   }
   __device__ __forceinline__ dwords4 read(const uint8_t* st, int i, int s) const {
     if constexpr (ALONG) {
-      return *reinterpret_cast<const dwords4*>(st + (base ^ (32 * s)) + i * 32 * kChunkRow);
+      return *reinterpret_cast<const dwords4*>(st + (base ^ (64 * s)) + i * 16 * kChunkRow);
     } else {
       typedef short v4i16 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) v4i16* LdsPtr;
-      const uint8_t* p = st + (base ^ (i * 64)) + s * 16 * B * 2;
+      const uint8_t* p = st + (base ^ (i * 32)) + s * 32 * B * 2;
       const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p));
       const auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p + 4 * B * 2));
       const dwords2 a = __builtin_bit_cast(dwords2, lo), b = __builtin_bit_cast(dwords2, hi);
@@ -156,6 +149,7 @@ struct Reader {
 template <typename S, Product P, typename T, typename TO>
 __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArgs p, int col_tiles) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[S::STAGES * S::kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t turn[S::kWaves * S::kScratch];
   __shared__ TileTable table;
   constexpr bool kAlongX = P != Product::kWeights, kAlongY = P == Product::kOut;
   const int lane = threadIdx.x & 63;
@@ -242,12 +236,21 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   int load_tile = 0;
   const uint32_t ring_at = lds_address(ring);
   uint32_t load_at = ring_at;
-  // Requests the next chunk and moves on, to the next tile behind a tile's last.
-  // Behind the last tile the loads have empty ranges (nothing is fetched), so that
-  // the number on their way is always the same.
-  auto load_next = [&]() {
-    sx.load(load_at, wave, load_left);
-    sy.load(load_at + S::kX, wave, load_left);
+  // Half of the next chunk's loads are requested at a time; the second half moves on,
+  // to the next tile behind a tile's last chunk.  Behind the last tile the loads have
+  // empty ranges (nothing is fetched), so that the number on their way is the same.
+  constexpr int kHalf = S::kLoads / 2;
+  auto prepare = [&]() {
+    sx.prepare(load_left);
+    sy.prepare(load_left);
+  };
+  auto load = [&](int i) {
+    if (i < S::kLoadX)
+      sx.load(load_at, wave, i);
+    else
+      sy.load(load_at + S::kX, wave, i - S::kLoadX);
+  };
+  auto move_on = [&]() {
     load_left -= kChunk;
     load_at = load_at == ring_at + (S::STAGES - 1) * S::kStage ? ring_at : load_at + S::kStage;
     if (load_left <= 0) {
@@ -261,91 +264,122 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   };
 
   // ---- products
-  const int col = lane & 31, g = lane >> 5;
+  const int col = lane & 15, g = lane >> 4;
   Reader<S::BM, kAlongX> rx;
   Reader<S::BN, kAlongY> ry;
-  rx.init(wm * S::MT * 32);
-  ry.init(wn * S::NT * 32);
-  f32x16 acc[S::NT][S::MT];
-  struct Step {
-    dwords4 x[S::MT], y[S::NT];
+  rx.init(wm * S::MT * 16);
+  ry.init(wn * S::NT * 16);
+  f32x4 acc[S::NT][S::MT];
+  constexpr int kRowsHalf = S::MT / 2;
+  struct Rows {
+    dwords4 f[kRowsHalf];
   };
-  auto read = [&](const uint8_t* st, int s) {
-    Step f;
-#pragma unroll
-    for (int j = 0; j < S::NT; ++j) f.y[j] = ry.read(st + S::kX, j, s);
-#pragma unroll
-    for (int i = 0; i < S::MT; ++i) f.x[i] = rx.read(st, i, s);
-    return f;
+  struct Columns {
+    dwords4 f[S::NT];
   };
-  auto multiply = [&](const Step& f) {
+  auto read_rows = [&](const uint8_t* st, int s, int half) {
+    Rows r;
 #pragma unroll
-    for (int i = 0; i < S::MT; ++i)
-#pragma unroll
-      for (int j = 0; j < S::NT; ++j) acc[j][i] = mfma32(T{}, f.y[j], f.x[i], acc[j][i]);
+    for (int i = 0; i < kRowsHalf; ++i) r.f[i] = rx.read(st, half * kRowsHalf + i, s);
+    return r;
   };
+  auto read_columns = [&](const uint8_t* st, int s) {
+    Columns r;
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j) r.f[j] = ry.read(st + S::kX, j, s);
+    return r;
+  };
+  // Half of the wave's rows by all of its columns.  The reads in front of these products
+  // stay in front of them: left alone, the compiler moves each next to its use, and the
+  // matrix units wait for LDS.  REQUEST >= 0 requests that half of the next chunk between
+  // the products: all of it behind the barrier at once keeps every wave from its products
+  // until the loads are taken.
+  auto multiply = [&](const Rows& x, const Columns& y, auto which, auto request) {
+    constexpr int W = decltype(which)::value, REQUEST = decltype(request)::value;
+    constexpr int kAll = kRowsHalf * S::NT;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kRowsHalf; ++i)
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) {
+        f32x4& c = acc[j][W * kRowsHalf + i];
+        c = mfma16(T{}, y.f[j], x.f[i], c);
+        const int n = i * S::NT + j;
+        if constexpr (REQUEST >= 0) {
+#pragma unroll
+          for (int l = n * kHalf / kAll; l < (n + 1) * kHalf / kAll; ++l) {
+            __builtin_amdgcn_sched_barrier(0);
+            load(REQUEST * kHalf + l);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::integral_constant<int, -1> kNone{};
+  constexpr std::integral_constant<int, 0> kFirst{};
+  constexpr std::integral_constant<int, 1> kSecond{};
+
   // Zeros, or what the output holds.
   auto begin = [&](const Tile& t) {
 #pragma unroll
     for (int j = 0; j < S::NT; ++j)
 #pragma unroll
-      for (int i = 0; i < S::MT; ++i) acc[j][i] = f32x16{};
+      for (int i = 0; i < S::MT; ++i) acc[j][i] = f32x4{};
     if constexpr (P == Product::kWeights) {
       if (!p.accumulate || t.depth == 0) return;
 #pragma unroll
       for (int i = 0; i < S::MT; ++i) {
-        const int row = t.i0 + (wm * S::MT + i) * 32 + col;
+        const int row = t.i0 + (wm * S::MT + i) * 16 + col;
         const auto* o = static_cast<const typename TO::bits*>(p.out) +
                         (static_cast<int64_t>(t.e) * p.N + min(row, p.N - 1)) * p.K;
 #pragma unroll
         for (int j = 0; j < S::NT; ++j)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int c = t.j0 + (wn * S::NT + j) * 32 + 8 * (r / 4) + 4 * g + r % 4;
+          for (int r = 0; r < 4; ++r) {
+            const int c = t.j0 + (wn * S::NT + j) * 16 + 4 * g + r;
             if (c < p.K) acc[j][i][r] = to_float(TO{}, o[c]);
           }
       }
     }
   };
 
-  // acc[j][i][4 q + r] is column 32 j' + 8 q + 4 g + r of row 32 i' + col.  Results
-  // turn in LDS, 32 rows x kTurn bytes of them at a time, so that eight neighbouring
-  // lanes store that many contiguous bytes of a row.  `turn` is this wave's place; a
-  // row's 16-byte slots are stored with their number xor a few bits of the row's.
-  auto store = [&](const Tile& t, uint8_t* turn) {
+  // acc[j][i][r] is column 16 j' + 4 g + r of row 16 i' + col.  Results turn in LDS, 16
+  // rows x kTurn bytes of them at a time, so that eight neighbouring lanes store that many
+  // contiguous bytes of a row.  `place` is this wave's; a row's 16-byte slots are stored
+  // with their number xor a few bits of the row's.
+  auto store = [&](const Tile& t, uint8_t* place) {
     if (P == Product::kWeights && p.accumulate && t.depth == 0) return;
     constexpr int kCols = S::kTurn / kBytes<TO>, kSlots = S::kTurn / 16, kRows = 64 / kSlots;
-    static_assert(S::NT * 32 % kCols == 0 || kCols % (S::NT * 32) == 0, "columns turn evenly");
-    constexpr int kWide = kCols < S::NT * 32 ? kCols : S::NT * 32;
+    constexpr int kWide = kCols < S::NT * 16 ? kCols : S::NT * 16;
+    static_assert(S::NT * 16 % kWide == 0, "columns turn evenly");
     auto slot = [](int row, int n) { return (n ^ row) & (kSlots - 1); };
     const int64_t out_ld = P == Product::kWeights ? p.K : p.out_ld;
     auto* out = static_cast<typename TO::bits*>(p.out) +
                 (P == Product::kWeights ? static_cast<int64_t>(t.e) * p.N * p.K : 0);
 #pragma unroll
     for (int i = 0; i < S::MT; ++i) {
-      const int row0 = t.i0 + (wm * S::MT + i) * 32;
+      const int row0 = t.i0 + (wm * S::MT + i) * 16;
       if (row0 >= t.i1) break;
 #pragma unroll
-      for (int c0 = 0; c0 < S::NT * 32; c0 += kWide) {
+      for (int c0 = 0; c0 < S::NT * 16; c0 += kWide) {
 #pragma unroll
-        for (int c = 0; c < kWide; c += 8) {  // columns c0 + c + 4 g ... + 3
-          f32x4 v;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = acc[(c0 + c) / 32][i][(c0 + c) % 32 / 2 + r];
+        for (int c = 0; c < kWide; c += 16) {  // columns c0 + c + 4 g ... + 3
+          const f32x4 v = acc[(c0 + c) / 16][i];
           const int at = (c + 4 * g) * kBytes<TO>;
-          uint8_t* to = turn + col * S::kTurn + slot(col, at >> 4) * 16;
+          uint8_t* to = place + col * S::kTurn + slot(col, at >> 4) * 16;
           if constexpr (kBytes<TO> == 4)
             *reinterpret_cast<dwords4*>(to) = __builtin_bit_cast(dwords4, v);
           else
             *reinterpret_cast<dwords2*>(to + (at & 8)) = pack4<TO>(v);
         }
         const int in = lane % kSlots * (16 / kBytes<TO>);
-        const int j = t.j0 + wn * S::NT * 32 + c0 + in;
+        const int j = t.j0 + wn * S::NT * 16 + c0 + in;
 #pragma unroll
-        for (int r = 0; r < 32; r += kRows) {
+        for (int r = 0; r < 16; r += kRows) {
           const int row = r + lane / kSlots;
           const dwords4 d =
-              *reinterpret_cast<const dwords4*>(turn + row * S::kTurn + slot(row, lane) * 16);
+              *reinterpret_cast<const dwords4*>(place + row * S::kTurn + slot(row, lane) * 16);
           if (row0 + row >= t.i1 || (kWide < kCols && in >= kWide)) continue;
           auto* o = out + (row0 + row) * out_ld + j;
           if (j + 16 / kBytes<TO> <= cols) {
@@ -364,36 +398,40 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
 
   aim(locate(0));
 #pragma unroll
-  for (int s = 0; s < S::STAGES; ++s) load_next();
-  wait_loads_and_barrier<(S::STAGES - 1) * S::kLoads>();
+  for (int s = 0; s < S::STAGES; ++s) {
+    prepare();
+#pragma unroll
+    for (int i = 0; i < (s + 1 < S::STAGES ? S::kLoads : kHalf); ++i) load(i);
+    if (s + 1 < S::STAGES) move_on();
+  }
+  wait_loads_and_barrier<(S::STAGES - 2) * S::kLoads + kHalf>();
   uint32_t stage = 0;
   Tile t = locate(0);
   int chunks = chunks_of(t);
   begin(t);
-  Step f = read(ring, 0);
+  Columns y = read_columns(ring, 0), y1;
+  Rows x = read_rows(ring, 0, 0), x1;
   for (int n = 0, c = 0;;) {
     const uint8_t* st = ring + stage;
-    Step f1 = read(st, 1);
-    multiply(f);
-    f = read(st, 2);
-    multiply(f1);
-    f1 = read(st, 3);
-    multiply(f);
+    x1 = read_rows(st, 0, 1);
+    multiply(x, y, kFirst, kSecond);
+    move_on();
+    y1 = read_columns(st, 1);
+    x = read_rows(st, 1, 0);
+    multiply(x1, y, kSecond, kNone);
+    x1 = read_rows(st, 1, 1);
+    multiply(x, y1, kFirst, kNone);
     // every wave holds its last fragments of this chunk; the next one is there when
     // only those behind it are on their way (stores among them make the wait
     // longer, never too short)
     wait_loads_and_barrier<(S::STAGES - 2) * S::kLoads>();
-    const uint32_t free = stage;
     stage = stage + S::kStage == S::STAGES * S::kStage ? 0 : stage + S::kStage;
-    const bool last = ++c == chunks;
-    if (!last) load_next();
-    f = read(ring + stage, 0);
-    multiply(f1);
-    if (!last) continue;
-    // results leave through the place that is free now, which is loaded after that
-    store(t, ring + free + wave * S::kScratch);
-    wait_lds_and_barrier();
-    load_next();
+    prepare();
+    y = read_columns(ring + stage, 0);
+    x = read_rows(ring + stage, 0, 0);
+    multiply(x1, y1, kSecond, kFirst);
+    if (++c < chunks) continue;
+    store(t, turn + wave * S::kScratch);
     if (++n == mine) break;
     t = locate(n);
     chunks = chunks_of(t);
