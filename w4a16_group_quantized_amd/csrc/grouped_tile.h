@@ -74,14 +74,15 @@ struct GroupedShape {
   static_assert(kLoads % 2 == 0 && MT % 2 == 0, "chunks are requested and rows multiplied in halves");
 };
 
-// One operand's way through memory: where the next chunk begins and how many bytes
-// there are from there (all uniform), and this lane's offset in a chunk.
+// One operand's way through memory: the range that begins with the next chunk (uniform),
+// and this lane's offset in a chunk.  What changes from chunk to chunk is a few scalar
+// steps: all waves take them between the same products.
 template <int B, int WAVES, bool ALONG>
 struct Stream {
   static constexpr int kLoad = B * kChunkRow / 1024 / WAVES;
-  const uint8_t* at;
-  int64_t left, step;
-  uint32_t lane_at, load_step;
+  Descriptor range;
+  uint32_t step, shrink;  // bytes to the next chunk, and what the range loses by it
+  uint32_t lane_at, load_step, from;
   int depth_at;  // ALONG: where in the chunk this lane's values lie
 
   static __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
@@ -94,24 +95,31 @@ struct Stream {
     const uint32_t row = u / kBlocks, blk = (u % kBlocks) ^ swizzle(row);
     lane_at = row * static_cast<uint32_t>(ld * 2) + blk * 16;
     load_step = WAVES * 64 / kBlocks * static_cast<uint32_t>(ld * 2);
-    depth_at = ALONG ? blk * 8 : 0;
-    step = ALONG ? kChunkRow : kChunk * ld * 2;
-  }
-  // The chunk that is requested next; `depth` values of the reduction are left.  Blocks
-  // behind it, and rows behind the tensor, become zeros.
-  Descriptor range;
-  uint32_t from;
-  __device__ __forceinline__ void prepare(int depth) {
-    const int64_t n = left < 0 ? 0 : left;
-    range = descriptor(at, static_cast<uint32_t>(n < INT32_MAX ? n : INT32_MAX));
     from = lane_at;
-    if (ALONG && depth < kChunk) from = depth_at < depth ? from : kOutOfRange;
-    at += step;
-    left -= step;
+    depth_at = ALONG ? blk * 8 : 0;
+    step = ALONG ? kChunkRow : static_cast<uint32_t>(kChunk * ld * 2);
   }
-  // Part i of it, into LDS from address `lds` on.
+  // `bytes` (under 2^31) from `at` on hold the tile's rows; with fixed, of every chunk.
+  __device__ __forceinline__ void aim(const uint16_t* at, int64_t bytes, bool fixed) {
+    range = descriptor(at, static_cast<uint32_t>(bytes));
+    shrink = fixed ? 0 : step;
+  }
+  // Nothing is fetched from here on.
+  __device__ __forceinline__ void stop() { range.d[2] = shrink = step = 0; }
+  // `depth` values of the reduction are left: blocks behind it become zeros, as rows
+  // behind the range do.
+  __device__ __forceinline__ void prepare(int depth) {
+    if (ALONG) from = depth_at < depth ? lane_at : kOutOfRange;
+  }
+  // Part i of the chunk, into LDS from address `lds` on.
   __device__ __forceinline__ void load(uint32_t lds, int wave, int i) const {
     load16_to_lds(range, lds + (i * WAVES + wave) * 1024, from + i * load_step);
+  }
+  __device__ __forceinline__ void move_on() {
+    const uint64_t at = (static_cast<uint64_t>(range.d[1]) << 32 | range.d[0]) + step;
+    range.d[0] = static_cast<uint32_t>(at);
+    range.d[1] = static_cast<uint32_t>(at >> 32);
+    range.d[2] -= shrink;
   }
 };
 
@@ -215,22 +223,23 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   sx.init(wave, p.x_ld);
   sy.init(wave, P == Product::kWeights ? p.y_ld : p.K);
   int load_left = 0;  // of the reduction
+  uint32_t tail_x = 0, tail_y = 0;  // kWeights: bytes that hold the last chunk's rows
   auto aim = [&](const Tile& t) {
     load_left = t.depth;
     if constexpr (P == Product::kWeights) {
-      // rows of the segment, each from the tile's first column to the matrix's last
-      const int64_t n = t.depth;
-      sx.at = reinterpret_cast<const uint8_t*>(p.x + t.r0 * p.x_ld + t.i0);
-      sx.left = n > 0 ? ((n - 1) * p.x_ld + p.N - t.i0) * 2 : 0;
-      sy.at = reinterpret_cast<const uint8_t*>(p.y + t.r0 * p.y_ld + t.j0);
-      sy.left = n > 0 ? ((n - 1) * p.y_ld + p.K - t.j0) * 2 : 0;
+      // Rows of the segment, each from the tile's first column to the matrix's last.  All
+      // chunks but the last have their 64 rows, whatever a row's end reads of the next.
+      const int64_t n = (t.depth - 1) % kChunk;
+      tail_x = t.depth > 0 ? static_cast<uint32_t>((n * p.x_ld + p.N - t.i0) * 2) : 0;
+      tail_y = t.depth > 0 ? static_cast<uint32_t>((n * p.y_ld + p.K - t.j0) * 2) : 0;
+      sx.aim(p.x + t.r0 * p.x_ld + t.i0, t.depth > kChunk ? INT32_MAX : tail_x, true);
+      sy.aim(p.y + t.r0 * p.y_ld + t.j0, t.depth > kChunk ? INT32_MAX : tail_y, true);
     } else {
-      sx.at = reinterpret_cast<const uint8_t*>(p.x + t.i0 * p.x_ld);
-      sx.left = (static_cast<int64_t>(t.i1 - t.i0 - 1) * p.x_ld + t.depth) * 2;
       const int64_t w = static_cast<int64_t>(p.N) * p.K;
       const int64_t skip = P == Product::kOut ? static_cast<int64_t>(t.j0) * p.K : t.j0;
-      sy.at = reinterpret_cast<const uint8_t*>(p.y + t.e * w + skip);
-      sy.left = (w - skip) * 2;
+      sx.aim(p.x + t.i0 * p.x_ld, (static_cast<int64_t>(t.i1 - t.i0 - 1) * p.x_ld + t.depth) * 2,
+             false);
+      sy.aim(p.y + t.e * w + skip, (w - skip) * 2, false);
     }
   };
   int load_tile = 0;
@@ -253,13 +262,20 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   auto move_on = [&]() {
     load_left -= kChunk;
     load_at = load_at == ring_at + (S::STAGES - 1) * S::kStage ? ring_at : load_at + S::kStage;
-    if (load_left <= 0) {
-      if (++load_tile < mine) {
-        aim(locate(load_tile));
-      } else {
-        sx.left = sy.left = 0;
-        load_left = INT32_MAX;
+    if (load_left > 0) {
+      sx.move_on();
+      sy.move_on();
+      if (P == Product::kWeights && load_left <= kChunk) {
+        sx.range.d[2] = tail_x;
+        sy.range.d[2] = tail_y;
       }
+    } else if (++load_tile < mine) {
+      aim(locate(load_tile));
+    } else {
+      sx.stop();
+      sy.stop();
+      load_left = INT32_MAX;
+      tail_x = tail_y = 0;
     }
   };
 
