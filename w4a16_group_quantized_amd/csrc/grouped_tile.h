@@ -49,12 +49,16 @@ __device__ __forceinline__ f32x4 mfma16(BF16, dwords4 a, dwords4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V, a),
                                                  __builtin_bit_cast(V, b), c, 0, 0, 0);
 }
-// Rows [r0, r1) of expert e, inside the tensors whatever the offsets hold.
+// Rows [r0, r1) of expert e, inside the tensors whatever the offsets hold.  The offsets
+// do not change while a kernel runs: loads through the scalar cache.
 __device__ __forceinline__ void segment(const GroupedArgs& p, int e, int& r0, int& r1) {
-  r0 = p.offsets == nullptr ? 0 : min(max(p.offsets[e], 0), p.rows);
-  r1 = p.offsets == nullptr ? p.rows : min(max(p.offsets[e + 1], 0), p.rows);
+  typedef const __attribute__((address_space(4))) int* Constants;
+  const auto o = (Constants)(p.offsets);
+  r0 = p.offsets == nullptr ? 0 : min(max(o[e], 0), p.rows);
+  r1 = p.offsets == nullptr ? p.rows : min(max(o[e + 1], 0), p.rows);
 }
 
+constexpr int kGroupTiles = 4;
 constexpr int kChunk = 64;      // of the reduction
 constexpr int kChunkRow = 128;  // bytes of it in a row
 
@@ -67,9 +71,11 @@ struct GroupedShape {
   static constexpr int kLoadX = kX / 1024 / kWaves, kLoadY = kY / 1024 / kWaves;
   static constexpr int kLoads = kLoadX + kLoadY;              // per wave and chunk
   static constexpr int kTurn = 128, kScratch = 16 * kTurn;    // results turn per wave, below
-  static constexpr int kLds = STAGES * kStage + kWaves * kScratch + static_cast<int>(sizeof(TileTable));
-  static constexpr int kPerCu = static_cast<int>(kGfx950LdsBytes) / kLds;
-  static_assert(kPerCu >= 1, "the ring fits in LDS");
+  static constexpr int per_cu(Product p) {
+    return static_cast<int>(kGfx950LdsBytes) /
+           (STAGES * kStage + kWaves * kScratch +
+            (p == Product::kWeights ? 0 : static_cast<int>(sizeof(TileTable))));
+  }
   static_assert(kLoadX * kWaves * 1024 == kX && kLoadY * kWaves * 1024 == kY, "loads divide evenly");
   static_assert(kLoads % 2 == 0 && MT % 2 == 0, "chunks are requested and rows multiplied in halves");
 };
@@ -155,7 +161,7 @@ struct Reader {
 };
 
 template <typename S, Product P, typename T, typename TO>
-__global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArgs p, int col_tiles) {
+__global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[S::STAGES * S::kStage];
   __shared__ __attribute__((aligned(16))) uint8_t turn[S::kWaves * S::kScratch];
   __shared__ TileTable table;
@@ -168,12 +174,10 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   // Tiles in groups of kGroupTiles row tiles, rows fastest, and each XCD (the
   // workgroups of equal index mod 8) a contiguous run of them: the tiles that run
   // together share both operands in its L2.
-  constexpr int kGroupTiles = 4;
-  const int w_tiles = (p.N + S::BM - 1) / S::BM;  // kWeights: row tiles of an expert
   const int total = P == Product::kWeights
-                        ? p.E * w_tiles
+                        ? p.E * p.row_tiles
                         : keep_tiles(count_tiles(p.offsets, p.E, p.rows, S::BM), table);
-  const int all = total * col_tiles;
+  const int all = total * p.col_tiles;
   const int run = (all + 7) >> 3;
   const int run0 = (blockIdx.x & 7) * run;
   const int run_n = min(run, all - run0);
@@ -184,34 +188,33 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
     int e, i0, i1, j0;  // rows [i0, i1) and columns from j0 on of the output
     int r0, depth;      // kWeights: first row of the segment; terms of the sums
   };
+  // Row and column tile of tile n of `rows` row tiles.
+  auto place = [&](int n, int rows, int& row, int& column) {
+    const int grp = p.by_group(n);
+    const int in = n - grp * kGroupTiles * p.col_tiles;
+    const int gm = min(kGroupTiles, rows - grp * kGroupTiles);
+    column = gm == 4 ? in >> 2 : gm == 2 ? in >> 1 : gm == 1 ? in : __umulhi(in, 0x55555556u);
+    row = grp * kGroupTiles + in - column * gm;
+  };
   auto locate = [&](int j) {
     const int tile = run0 + first_tile + j * step;
     Tile t;
+    int row, column;
     if constexpr (P == Product::kWeights) {
-      const int per = w_tiles * col_tiles;
-      t.e = tile / per;
-      const int at = tile - t.e * per;
-      const int grp = at / (kGroupTiles * col_tiles);
-      const int in = at - grp * kGroupTiles * col_tiles;
-      const int gm = min(kGroupTiles, w_tiles - grp * kGroupTiles);
-      const int nt = in / gm;
-      t.i0 = (grp * kGroupTiles + in - nt * gm) * S::BM;
+      t.e = p.by_expert(tile);
+      place(tile - t.e * p.row_tiles * p.col_tiles, p.row_tiles, row, column);
+      t.i0 = row * S::BM;
       t.i1 = min(p.N, t.i0 + S::BM);
-      t.j0 = nt * S::BN;
       int r1;
       segment(p, t.e, t.r0, r1);
       t.depth = max(r1 - t.r0, 0);
     } else {
-      const int grp = tile / (kGroupTiles * col_tiles);
-      const int in = tile - grp * kGroupTiles * col_tiles;
-      const int gm = min(kGroupTiles, total - grp * kGroupTiles);
-      const int nt = in / gm;
-      t.j0 = nt * S::BN;
-      find_tile(kept_tiles(table, p.offsets, p.E, p.rows, S::BM, total),
-                grp * kGroupTiles + in - nt * gm, t.e, t.i0, t.i1);
+      place(tile, total, row, column);
+      find_tile(kept_tiles(table, p.offsets, p.E, p.rows, S::BM, total), row, t.e, t.i0, t.i1);
       t.r0 = 0;
       t.depth = P == Product::kOut ? p.K : p.N;
     }
+    t.j0 = column * S::BN;
     return t;
   };
   // an expert without rows still has a chunk (of zeros)
@@ -310,27 +313,40 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   // matrix units wait for LDS.  REQUEST >= 0 requests that half of the next chunk between
   // the products: all of it behind the barrier at once keeps every wave from its products
   // until the loads are taken.
-  auto multiply = [&](const Rows& x, const Columns& y, auto which, auto request) {
+  auto multiply = [&](const Rows& x, const Columns& y, auto which, auto request, bool on) {
     constexpr int W = decltype(which)::value, REQUEST = decltype(request)::value;
     constexpr int kAll = kRowsHalf * S::NT;
     __builtin_amdgcn_sched_barrier(0);
+    if (on) {
 #pragma unroll
-    for (int i = 0; i < kRowsHalf; ++i)
+      for (int i = 0; i < kRowsHalf; ++i)
 #pragma unroll
-      for (int j = 0; j < S::NT; ++j) {
-        f32x4& c = acc[j][W * kRowsHalf + i];
-        c = mfma16(T{}, y.f[j], x.f[i], c);
-        const int n = i * S::NT + j;
-        if constexpr (REQUEST >= 0) {
+        for (int j = 0; j < S::NT; ++j) {
+          f32x4& c = acc[j][W * kRowsHalf + i];
+          c = mfma16(T{}, y.f[j], x.f[i], c);
+          const int n = i * S::NT + j;
+          if constexpr (REQUEST >= 0) {
 #pragma unroll
-          for (int l = n * kHalf / kAll; l < (n + 1) * kHalf / kAll; ++l) {
-            __builtin_amdgcn_sched_barrier(0);
-            load(REQUEST * kHalf + l);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int l = n * kHalf / kAll; l < (n + 1) * kHalf / kAll; ++l) {
+              __builtin_amdgcn_sched_barrier(0);
+              load(REQUEST * kHalf + l);
+              __builtin_amdgcn_sched_barrier(0);
+            }
           }
         }
-      }
+    } else if constexpr (REQUEST >= 0) {
+#pragma unroll
+      for (int l = 0; l < kHalf; ++l) load(REQUEST * kHalf + l);
+    }
     __builtin_amdgcn_sched_barrier(0);
+  };
+  // Whether half W of this wave's rows has any that is stored: the others' products are
+  // left out, and so are those of a chunk's second step behind the reduction's end (8
+  // experts of 8192 x 4096, 16381 rows: 1001 -> 975 us).  Not in the gradient of the
+  // weights, whose tiles are whole but at the matrix's edge: 8192 cubed 769 us, with the
+  // branches 798.
+  auto has_rows = [&](const Tile& t, int W) {
+    return P == Product::kWeights || t.i0 + (wm * S::MT + W * kRowsHalf) * 16 < t.i1;
   };
   constexpr std::integral_constant<int, -1> kNone{};
   constexpr std::integral_constant<int, 0> kFirst{};
@@ -364,8 +380,8 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   // rows x kTurn bytes of them at a time, so that eight neighbouring lanes store that many
   // contiguous bytes of a row.  `place` is this wave's; a row's 16-byte slots are stored
   // with their number xor a few bits of the row's.
-  auto store = [&](const Tile& t, uint8_t* place) {
-    if (P == Product::kWeights && p.accumulate && t.depth == 0) return;
+  auto store = [&](const Tile& t, uint8_t* place, auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;  // every row and column is there
     constexpr int kCols = S::kTurn / kBytes<TO>, kSlots = S::kTurn / 16, kRows = 64 / kSlots;
     constexpr int kWide = kCols < S::NT * 16 ? kCols : S::NT * 16;
     static_assert(S::NT * 16 % kWide == 0, "columns turn evenly");
@@ -376,7 +392,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
 #pragma unroll
     for (int i = 0; i < S::MT; ++i) {
       const int row0 = t.i0 + (wm * S::MT + i) * 16;
-      if (row0 >= t.i1) break;
+      if (!WHOLE && row0 >= t.i1) break;
 #pragma unroll
       for (int c0 = 0; c0 < S::NT * 16; c0 += kWide) {
 #pragma unroll
@@ -396,9 +412,10 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
           const int row = r + lane / kSlots;
           const dwords4 d =
               *reinterpret_cast<const dwords4*>(place + row * S::kTurn + slot(row, lane) * 16);
-          if (row0 + row >= t.i1 || (kWide < kCols && in >= kWide)) continue;
+          if (kWide < kCols && in >= kWide) continue;
+          if (!WHOLE && row0 + row >= t.i1) continue;
           auto* o = out + (row0 + row) * out_ld + j;
-          if (j + 16 / kBytes<TO> <= cols) {
+          if (WHOLE || j + 16 / kBytes<TO> <= cols) {
             store16(o, d);
           } else {
 #pragma unroll
@@ -427,16 +444,18 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   begin(t);
   Columns y = read_columns(ring, 0), y1;
   Rows x = read_rows(ring, 0, 0), x1;
+  bool first = has_rows(t, 0), second = has_rows(t, 1);
   for (int n = 0, c = 0;;) {
+    const bool more = P == Product::kWeights || t.depth - c * kChunk > kChunk / 2;
     const uint8_t* st = ring + stage;
     x1 = read_rows(st, 0, 1);
-    multiply(x, y, kFirst, kSecond);
+    multiply(x, y, kFirst, kSecond, first);
     move_on();
     y1 = read_columns(st, 1);
     x = read_rows(st, 1, 0);
-    multiply(x1, y, kSecond, kNone);
+    multiply(x1, y, kSecond, kNone, second);
     x1 = read_rows(st, 1, 1);
-    multiply(x, y1, kFirst, kNone);
+    multiply(x, y1, kFirst, kNone, first && more);
     // every wave holds its last fragments of this chunk; the next one is there when
     // only those behind it are on their way (stores among them make the wait
     // longer, never too short)
@@ -445,13 +464,21 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
     prepare();
     y = read_columns(ring + stage, 0);
     x = read_rows(ring + stage, 0, 0);
-    multiply(x1, y1, kSecond, kFirst);
+    multiply(x1, y1, kSecond, kFirst, second && more);
     if (++c < chunks) continue;
-    store(t, turn + wave * S::kScratch);
+    if (P == Product::kWeights && p.accumulate && t.depth == 0) {
+      // stays as it is
+    } else if (t.i1 - t.i0 == S::BM && t.j0 + S::BN <= cols) {
+      store(t, turn + wave * S::kScratch, std::true_type{});
+    } else {
+      store(t, turn + wave * S::kScratch, std::false_type{});
+    }
     if (++n == mine) break;
     t = locate(n);
     chunks = chunks_of(t);
     c = 0;
+    first = has_rows(t, 0);
+    second = has_rows(t, 1);
     begin(t);
   }
   // no load into this workgroup's LDS outlives it
@@ -472,17 +499,22 @@ void with_types(const GroupedArgs& a, F&& f) {
 template <typename S, Product P>
 void launch_grouped_tiles(const GroupedArgs& a, hipStream_t stream) {
   const int cols = P == Product::kOut ? a.N : a.K;
-  const int col_tiles = (cols + S::BN - 1) / S::BN;
+  GroupedArgs args = a;
+  args.row_tiles = (a.N + S::BM - 1) / S::BM;
+  args.col_tiles = (cols + S::BN - 1) / S::BN;
+  args.by_expert = Divisor(args.row_tiles * args.col_tiles);
+  args.by_group = Divisor(kGroupTiles * args.col_tiles);
   // at most one short tile per expert; no more workgroups than run at once
   const int64_t row_tiles =
-      P == Product::kWeights ? static_cast<int64_t>(a.E) * ((a.N + S::BM - 1) / S::BM)
+      P == Product::kWeights ? static_cast<int64_t>(a.E) * args.row_tiles
                              : a.rows / S::BM + (a.E < a.rows ? a.E : a.rows);
-  const int64_t resident = static_cast<int64_t>(device_info().cus) * S::kPerCu;
-  const int64_t groups = row_tiles * col_tiles < resident ? row_tiles * col_tiles : resident;
+  const int64_t resident = static_cast<int64_t>(device_info().cus) * S::per_cu(P);
+  static_assert(S::per_cu(P) >= 1, "the ring fits in LDS");
+  const int64_t tiles = row_tiles * args.col_tiles, groups = tiles < resident ? tiles : resident;
   const dim3 grid(static_cast<unsigned>((groups + 7) / 8 * 8)), block(64 * S::kWaves);
   with_types(a, [&](auto t, auto to) {
     hipLaunchKernelGGL((grouped_tile_kernel<S, P, decltype(t), decltype(to)>), grid, block, 0,
-                       stream, a, col_tiles);
+                       stream, args);
   });
 }
 

@@ -13,6 +13,24 @@ namespace moe {
 //   kWeights  grad_w[e, n, k] columns of grad x columns of a    over the expert's rows
 enum class Product { kOut, kRows, kWeights };
 
+// Division of 0 <= n < 2^31 by a number known at the launch: with 2^(c-1) < d <= 2^c and
+// mul = ceil(2^(31+c) / d) < 2^32, n mul exceeds n 2^(31+c) / d by less than n d / d < 2^31
+// <= 2^(31+c) / d, so its part above 2^(31+c) is n / d cut to an integer.
+struct Divisor {
+  uint32_t mul, shift;  // mul == 0: by 1
+  Divisor() = default;
+  explicit Divisor(uint32_t d) : mul(0), shift(0) {
+    uint32_t c = 0;
+    while ((1u << c) < d) ++c;
+    if (c == 0) return;
+    mul = static_cast<uint32_t>(((static_cast<uint64_t>(1) << (31 + c)) + d - 1) / d);
+    shift = c - 1;
+  }
+  __host__ __device__ uint32_t operator()(uint32_t n) const {
+    return mul == 0 ? n : static_cast<uint32_t>((static_cast<uint64_t>(n) * mul) >> 32) >> shift;
+  }
+};
+
 struct GroupedArgs {
   const uint16_t* x;  // a (kOut) or grad: [rows, ...], row stride x_ld
   int64_t x_ld;
@@ -26,6 +44,9 @@ struct GroupedArgs {
   int64_t out_ld;     // kOut, kRows
   int accumulate;     // kWeights: added to what out holds
   float* partial;     // kWeights: workspace of grouped_workspace_bytes
+  // set at the launch
+  int row_tiles, col_tiles;  // row_tiles: of an expert, kWeights only
+  Divisor by_expert, by_group;
 };
 size_t grouped_workspace_bytes(int64_t rows, int E, int N, int K);
 // With tiles of 16-byte loads (grouped_out.hip, grouped_rows.hip, grouped_weights.hip).
