@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -1217,40 +1218,58 @@ def moe_adamw(params: list, grads: list, m: list, v: list, *, lr: float, beta1: 
         return
     bits = 8 if isinstance(m[0], tuple) else 32
     dev = params[0].get_device()
-    table = []
-
-    def flat(name, i, t, n, dtype):
-        if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
-            raise ValueError(f"{name}[{i}] must be contiguous {dtype} of {n} elements on {params[0].device}, "
-                             f"is {t.dtype} of shape {tuple(t.shape)} on {t.device}")
-        return t.data_ptr()
-
-    def typed(name, i, t, n):
-        code = _DTYPE.get(t.dtype)
-        if code is None:
-            raise ValueError(f"{name}[{i}] is {t.dtype}, not float32, float16 or bfloat16")
-        return flat(name, i, t, n, t.dtype), code
-
-    for i in range(count):
-        p, mi, vi = params[i], m[i], v[i]
-        n = p.numel()
-        pp, p_code = typed("params", i, p, n)
-        pg, g_code = typed("grads", i, grads[i], n)
-        pc, c_code = (0, 0) if copies is None or copies[i] is None else typed("copies", i, copies[i], n)
-        if (isinstance(mi, tuple), isinstance(vi, tuple)) != (bits == 8, bits == 8):
-            raise ValueError(f"m[{i}] and v[{i}] are not states of {bits} bits as m[0] is")
-        if bits == 32:
-            states = (flat("m", i, mi, n, torch.float32), flat("v", i, vi, n, torch.float32), 0, 0)
-        else:
-            blocks = (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
-            states = (flat("m", i, mi[0], n, torch.uint8), flat("v", i, vi[0], n, torch.uint8),
-                      flat("m scales", i, mi[1], blocks, torch.float32),
-                      flat("v scales", i, vi[1], blocks, torch.float32))
-        table += (n, pp, pg, *states, pc, p_code | g_code << 32, c_code)
-    scale = None if grad_scale is None else _dense("grad_scale", grad_scale, torch.float32, 1)
-    if scale is not None:
+    if dev < 0 or grad_scale is not None:
         _device_of(params[0], grad_scale)
-    elif dev < 0:
-        _device_of(params[0])
-    _run("moe_adamw", dev, (ctypes.c_int64 * len(table))(*table), count, bits, lr, beta1, beta2, eps,
-         weight_decay, step, seed & 0xFFFFFFFF, scale)
+
+    # a column of the table: one loop over a list's tensors, which asks each as little as it can
+    def column(name, tensors, sizes, dtype):
+        ptrs = []
+        add = ptrs.append
+        for t, n in zip(tensors, sizes):
+            if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+                raise ValueError(f"{name}[{len(ptrs)}] must be contiguous {dtype} of {n} elements on "
+                                 f"{params[0].device}, is {t.dtype} of shape {tuple(t.shape)} on {t.device}")
+            add(t.data_ptr())
+        return ptrs
+
+    def typed(name, tensors, sizes):
+        kinds = {t.dtype for t in tensors}
+        if len(kinds) == 1:
+            dtype = kinds.pop()
+            if dtype in _DTYPE:
+                return column(name, tensors, sizes, dtype), [_DTYPE[dtype]] * count
+        for i, t in enumerate(tensors):
+            if t.dtype not in _DTYPE:
+                raise ValueError(f"{name}[{i}] is {t.dtype}, not float32, float16 or bfloat16")
+        return ([column(f"{name}, from {i} on", [t], [n], t.dtype)[0]
+                 for i, (t, n) in enumerate(zip(tensors, sizes))], [_DTYPE[t.dtype] for t in tensors])
+
+    ns = [p.numel() for p in params]
+    pp, p_codes = typed("params", params, ns)
+    pg, g_codes = typed("grads", grads, ns)
+    none = [0] * count
+    if any([isinstance(x, tuple) != (bits == 8) for x in m]) or any([isinstance(x, tuple) != (bits == 8) for x in v]):
+        raise ValueError(f"m and v are not all states of {bits} bits as m[0] is")
+    if bits == 32:
+        pm, pv = column("m", m, ns, torch.float32), column("v", v, ns, torch.float32)
+        ms = vs = none
+    else:
+        blocks = [(n + ADAMW_BLOCK - 1) // ADAMW_BLOCK for n in ns]
+        (mc, ms), (vc, vs) = zip(*m), zip(*v)
+        pm, pv = column("m codes", mc, ns, torch.uint8), column("v codes", vc, ns, torch.uint8)
+        ms, vs = column("m scales", ms, blocks, torch.float32), column("v scales", vs, blocks, torch.float32)
+    pc, c_codes = none, none
+    if copies is not None:
+        at = [i for i, c in enumerate(copies) if c is not None]
+        if len(at) == count:
+            pc, c_codes = typed("copies", copies, ns)
+        else:
+            pc, c_codes = list(none), list(none)
+            for i in at:
+                (pc[i],), (code, *_) = typed("copies", [copies[i]], [ns[i]])
+                c_codes[i] = code
+    scale = None if grad_scale is None else _dense("grad_scale", grad_scale, torch.float32, 1)
+    kinds = p_codes if g_codes == none else [a | b << 32 for a, b in zip(p_codes, g_codes)]
+    table = [x for row in zip(ns, pp, pg, pm, pv, ms, vs, pc, kinds, c_codes) for x in row]
+    _run("moe_adamw", dev, struct.pack(f"{10 * count}q", *table), count, bits, lr, beta1, beta2, eps, weight_decay,
+         step, seed & 0xFFFFFFFF, scale)
