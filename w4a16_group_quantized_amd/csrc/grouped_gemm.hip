@@ -129,8 +129,6 @@ void launch_any(const GroupedArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-size_t grouped_workspace_bytes(int64_t, int, int, int) { return 0; }
-
 // What the tile kernels' 16-byte loads and 32-bit offsets take.
 static bool tiles_take(Product p, const GroupedArgs& a) {
   auto whole = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; };

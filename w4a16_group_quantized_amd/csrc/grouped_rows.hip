@@ -3,15 +3,19 @@
 
 namespace moe {
 
+// The rules go by the mean rows per expert; their figures are of rows shared out evenly.
 void launch_grouped_rows(const GroupedArgs& a, hipStream_t stream) {
-  // by the mean rows per expert; 8 experts of 8192 x 4096, 16381 rows:
-  // 1075 us, with tiles of 128 x 128 1308; 512 of 2560 x 640, 40960 rows: 431 and 336
-  const int active = a.E < a.rows ? a.E : a.rows;
+  const int active = a.E < a.rows ? a.E : a.rows;  // experts that can hold a row
   const int mean = a.rows / active;
-  const int64_t tiles = static_cast<int64_t>(active) * ((mean + 255) / 256) * ((a.K + 255) / 256);
-  if (mean >= 256 && tiles >= device_info().cus)
-    return launch_grouped_tiles<Grouped256, Product::kRows>(a, stream);
-  launch_grouped_tiles<Grouped128, Product::kRows>(a, stream);
+  const auto tiles = [&](int size) { return row_product_tiles(active, mean, a.K, size); };
+  // 1 expert of 4096 x 512, 100 rows: 64 tiles of 32 x 32 with eight waves each 10.5 us,
+  // 16 of 64 x 64 26.5; 8 experts of 2560 x 640, 1000 rows, 640 tiles 27.9 and 160 18.4
+  if (tiles(32) <= kUnits)
+    return launch_grouped_tiles<GroupedSplit, Product::kRows>(a, stream);
+  const int size = pick_size(tiles);
+  if (size == 256) return launch_grouped_tiles<Grouped256, Product::kRows>(a, stream);
+  if (size == 128) return launch_grouped_tiles<Grouped128, Product::kRows>(a, stream);
+  launch_grouped_tiles<Grouped64, Product::kRows>(a, stream);
 }
 
 }  // namespace moe

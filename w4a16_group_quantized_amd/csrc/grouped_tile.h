@@ -62,28 +62,35 @@ constexpr int kGroupTiles = 4;
 constexpr int kChunk = 64;      // of the reduction
 constexpr int kChunkRow = 128;  // bytes of it in a row
 
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
+// KS > 1 groups of WM x WN waves take KS chunks at once, one each, and add their sums in
+// LDS at a tile's end, in a fixed order: few tiles of a long reduction then have KS times
+// as many waves at work, and a barrier for KS chunks.
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int KS_ = 1>
 struct GroupedShape {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
-  static constexpr int kWaves = WM * WN;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_, KS = KS_;
+  static constexpr int kGroup = WM * WN, kWaves = KS * kGroup;
+  static constexpr int kDepth = KS * kChunk;                 // of the reduction per stage
   static constexpr int MT = BM / 16 / WM, NT = BN / 16 / WN;  // 16 x 16 results per wave
-  static constexpr int kX = BM * kChunkRow, kY = BN * kChunkRow, kStage = kX + kY;
-  static constexpr int kLoadX = kX / 1024 / kWaves, kLoadY = kY / 1024 / kWaves;
-  static constexpr int kLoads = kLoadX + kLoadY;              // per wave and chunk
+  static constexpr int kX = BM * kChunkRow, kY = BN * kChunkRow, kPart = kX + kY;
+  static constexpr int kStage = KS * kPart;
+  static constexpr int kLoadX = kX / 1024 / kGroup, kLoadY = kY / 1024 / kGroup;
+  static constexpr int kLoads = kLoadX + kLoadY;              // per wave and stage
   static constexpr int kTurn = 128, kScratch = 16 * kTurn;    // results turn per wave, below
+  static constexpr int kSums = KS / 2 * BM * BN * 4;          // of half of the groups
   static constexpr int per_cu(Product p) {
     return static_cast<int>(kGfx950LdsBytes) /
-           (STAGES * kStage + kWaves * kScratch +
+           (STAGES * kStage + kGroup * kScratch + kSums +
             (p == Product::kWeights ? 0 : static_cast<int>(sizeof(TileTable))));
   }
-  static_assert(kLoadX * kWaves * 1024 == kX && kLoadY * kWaves * 1024 == kY, "loads divide evenly");
-  static_assert(kLoads % 2 == 0 && MT % 2 == 0, "chunks are requested and rows multiplied in halves");
+  static_assert(kLoadX * kGroup * 1024 == kX && kLoadY * kGroup * 1024 == kY, "loads divide evenly");
+  static_assert(kLoads >= 2 && MT % 2 == 0, "chunks are requested and rows multiplied in halves");
+  static_assert((KS & (KS - 1)) == 0, "sums are added in halves");
 };
 
 // One operand's way through memory: the range that begins with the next chunk (uniform),
 // and this lane's offset in a chunk.  What changes from chunk to chunk is a few scalar
 // steps: all waves take them between the same products.
-template <int B, int WAVES, bool ALONG>
+template <int B, int WAVES, bool ALONG, int KS>
 struct Stream {
   static constexpr int kLoad = B * kChunkRow / 1024 / WAVES;
   Descriptor range;
@@ -92,18 +99,22 @@ struct Stream {
   int depth_at;  // ALONG: where in the chunk this lane's values lie
 
   static __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
-    return ALONG ? (row >> 1) & 7 : ((row & 3) << 2) | ((row >> 2) & 2);
+    // the same for all of a lane's loads, WAVES * 8 rows apart
+    if (ALONG) return WAVES > 1 ? (row >> 1) & 7 : row & 7;
+    return B >= 128 ? ((row & 3) << 2) | ((row >> 2) & 2) : B == 64 ? (row & 3) << 1 : (row & 1) << 1;
   }
-  __device__ __forceinline__ void init(int wave, int64_t ld) {
+  // `part`: which of the stage's chunks this wave takes.
+  __device__ __forceinline__ void init(int wave, int part, int64_t ld) {
     const uint32_t u = wave * 64 + (threadIdx.x & 63);
     constexpr uint32_t kBlocks = ALONG ? 8 : B / 8;  // of 16 bytes per row in LDS
-    static_assert(ALONG || kBlocks >= 16, "the swizzle stays inside a row");
+    static_assert(ALONG || kBlocks >= 4, "the swizzle stays inside a row");
     const uint32_t row = u / kBlocks, blk = (u % kBlocks) ^ swizzle(row);
-    lane_at = row * static_cast<uint32_t>(ld * 2) + blk * 16;
+    const uint32_t chunk = ALONG ? kChunkRow : static_cast<uint32_t>(kChunk * ld * 2);
+    lane_at = part * chunk + row * static_cast<uint32_t>(ld * 2) + blk * 16;
     load_step = WAVES * 64 / kBlocks * static_cast<uint32_t>(ld * 2);
     from = lane_at;
-    depth_at = ALONG ? blk * 8 : 0;
-    step = ALONG ? kChunkRow : static_cast<uint32_t>(kChunk * ld * 2);
+    depth_at = ALONG ? part * kChunk + blk * 8 : 0;
+    step = KS * chunk;
   }
   // `bytes` (under 2^31) from `at` on hold the tile's rows; with fixed, of every chunk.
   __device__ __forceinline__ void aim(const uint16_t* at, int64_t bytes, bool fixed) {
@@ -131,17 +142,17 @@ struct Stream {
 
 // What a lane reads of an operand: fragment i (16 rows or columns), step s (32 of the
 // reduction) of the chunk at `st`.
-template <int B, bool ALONG>
+template <int B, int WAVES, bool ALONG>
 struct Reader {
   uint32_t base;
   __device__ __forceinline__ void init(int first) {  // the wave's first row or column
     const uint32_t l = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
     if constexpr (ALONG) {
       const uint32_t row = first + l;
-      base = row * kChunkRow + (g ^ ((row >> 1) & 7)) * 16;
+      base = row * kChunkRow + (g ^ Stream<B, WAVES, true, 1>::swizzle(row)) * 16;
     } else {
       const uint32_t q = g * 8 + (l >> 2), c = first + (l & 3) * 4;
-      const uint32_t blk = (c >> 3) ^ Stream<B, 1, false>::swizzle(q);
+      const uint32_t blk = (c >> 3) ^ Stream<B, WAVES, false, 1>::swizzle(q);
       base = q * (B * 2) + blk * 16 + (c & 4) * 2;
     }
   }
@@ -163,19 +174,21 @@ struct Reader {
 template <typename S, Product P, typename T, typename TO>
 __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[S::STAGES * S::kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t turn[S::kWaves * S::kScratch];
+  __shared__ __attribute__((aligned(16))) uint8_t turn[S::kGroup * S::kScratch];
+  __shared__ __attribute__((aligned(16))) uint8_t sums[S::kSums > 0 ? S::kSums : 16];
   __shared__ TileTable table;
   constexpr bool kAlongX = P != Product::kWeights, kAlongY = P == Product::kOut;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int part = wave / S::kGroup, in_group = wave % S::kGroup;
+  const int wm = in_group / S::WN, wn = in_group % S::WN;
   const int cols = P == Product::kOut ? p.N : p.K;
 
   // Tiles in groups of kGroupTiles row tiles, rows fastest, and each XCD (the
   // workgroups of equal index mod 8) a contiguous run of them: the tiles that run
   // together share both operands in its L2.
   const int total = P == Product::kWeights
-                        ? p.E * p.row_tiles
+                        ? p.E * p.parts * p.row_tiles
                         : keep_tiles(count_tiles(p.offsets, p.E, p.rows, S::BM), table);
   const int all = total * p.col_tiles;
   const int run = (all + 7) >> 3;
@@ -185,8 +198,8 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   if (first_tile >= run_n) return;
   const int mine = (run_n - first_tile + step - 1) / step;
   struct Tile {
-    int e, i0, i1, j0;  // rows [i0, i1) and columns from j0 on of the output
-    int r0, depth;      // kWeights: first row of the segment; terms of the sums
+    int e, i0, i1, j0;  // rows [i0, i1) and columns from j0 on of the output (of block e)
+    int r0, depth;      // kWeights: first row of the sums; how many terms they have
   };
   // Row and column tile of tile n of `rows` row tiles.
   auto place = [&](int n, int rows, int& row, int& column) {
@@ -205,8 +218,15 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
       place(tile - t.e * p.row_tiles * p.col_tiles, p.row_tiles, row, column);
       t.i0 = row * S::BM;
       t.i1 = min(p.N, t.i0 + S::BM);
+      const int e = p.by_parts(t.e);
       int r1;
-      segment(p, t.e, t.r0, r1);
+      segment(p, e, t.r0, r1);
+      if (p.parts > 1) {  // whole chunks to each part but the last
+        const int len = (p.by_parts(max(r1 - t.r0, 0) + p.parts - 1) + kChunk - 1) / kChunk * kChunk;
+        const int64_t from = t.r0 + static_cast<int64_t>(t.e - e * p.parts) * len;
+        t.r0 = static_cast<int>(min(from, static_cast<int64_t>(r1)));
+        r1 = min(r1, static_cast<int>(min(from + len, static_cast<int64_t>(INT32_MAX))));
+      }
       t.depth = max(r1 - t.r0, 0);
     } else {
       place(tile, total, row, column);
@@ -218,25 +238,25 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
     return t;
   };
   // an expert without rows still has a chunk (of zeros)
-  auto chunks_of = [](const Tile& t) { return max(1, (t.depth + kChunk - 1) / kChunk); };
+  auto chunks_of = [](const Tile& t) { return max(1, (t.depth + S::kDepth - 1) / S::kDepth); };
 
   // ---- loads: the tile and chunk that are requested next
-  Stream<S::BM, S::kWaves, kAlongX> sx;
-  Stream<S::BN, S::kWaves, kAlongY> sy;
-  sx.init(wave, p.x_ld);
-  sy.init(wave, P == Product::kWeights ? p.y_ld : p.K);
+  Stream<S::BM, S::kGroup, kAlongX, S::KS> sx;
+  Stream<S::BN, S::kGroup, kAlongY, S::KS> sy;
+  sx.init(in_group, part, p.x_ld);
+  sy.init(in_group, part, P == Product::kWeights ? p.y_ld : p.K);
   int load_left = 0;  // of the reduction
   uint32_t tail_x = 0, tail_y = 0;  // kWeights: bytes that hold the last chunk's rows
   auto aim = [&](const Tile& t) {
     load_left = t.depth;
     if constexpr (P == Product::kWeights) {
       // Rows of the segment, each from the tile's first column to the matrix's last.  All
-      // chunks but the last have their 64 rows, whatever a row's end reads of the next.
-      const int64_t n = (t.depth - 1) % kChunk;
+      // stages but the last have all their rows, whatever a row's end reads of the next.
+      const int64_t n = (t.depth - 1) % S::kDepth;
       tail_x = t.depth > 0 ? static_cast<uint32_t>((n * p.x_ld + p.N - t.i0) * 2) : 0;
       tail_y = t.depth > 0 ? static_cast<uint32_t>((n * p.y_ld + p.K - t.j0) * 2) : 0;
-      sx.aim(p.x + t.r0 * p.x_ld + t.i0, t.depth > kChunk ? INT32_MAX : tail_x, true);
-      sy.aim(p.y + t.r0 * p.y_ld + t.j0, t.depth > kChunk ? INT32_MAX : tail_y, true);
+      sx.aim(p.x + t.r0 * p.x_ld + t.i0, t.depth > S::kDepth ? INT32_MAX : tail_x, true);
+      sy.aim(p.y + t.r0 * p.y_ld + t.j0, t.depth > S::kDepth ? INT32_MAX : tail_y, true);
     } else {
       const int64_t w = static_cast<int64_t>(p.N) * p.K;
       const int64_t skip = P == Product::kOut ? static_cast<int64_t>(t.j0) * p.K : t.j0;
@@ -251,24 +271,24 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   // Half of the next chunk's loads are requested at a time; the second half moves on,
   // to the next tile behind a tile's last chunk.  Behind the last tile the loads have
   // empty ranges (nothing is fetched), so that the number on their way is the same.
-  constexpr int kHalf = S::kLoads / 2;
+  constexpr int kHalf = S::kLoads / 2;  // the first one, the smaller if they differ
   auto prepare = [&]() {
     sx.prepare(load_left);
     sy.prepare(load_left);
   };
   auto load = [&](int i) {
     if (i < S::kLoadX)
-      sx.load(load_at, wave, i);
+      sx.load(load_at + part * S::kPart, in_group, i);
     else
-      sy.load(load_at + S::kX, wave, i - S::kLoadX);
+      sy.load(load_at + part * S::kPart + S::kX, in_group, i - S::kLoadX);
   };
   auto move_on = [&]() {
-    load_left -= kChunk;
+    load_left -= S::kDepth;
     load_at = load_at == ring_at + (S::STAGES - 1) * S::kStage ? ring_at : load_at + S::kStage;
     if (load_left > 0) {
       sx.move_on();
       sy.move_on();
-      if (P == Product::kWeights && load_left <= kChunk) {
+      if (P == Product::kWeights && load_left <= S::kDepth) {
         sx.range.d[2] = tail_x;
         sy.range.d[2] = tail_y;
       }
@@ -284,8 +304,8 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
 
   // ---- products
   const int col = lane & 15, g = lane >> 4;
-  Reader<S::BM, kAlongX> rx;
-  Reader<S::BN, kAlongY> ry;
+  Reader<S::BM, S::kGroup, kAlongX> rx;
+  Reader<S::BN, S::kGroup, kAlongY> ry;
   rx.init(wm * S::MT * 16);
   ry.init(wn * S::NT * 16);
   f32x4 acc[S::NT][S::MT];
@@ -316,6 +336,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   auto multiply = [&](const Rows& x, const Columns& y, auto which, auto request, bool on) {
     constexpr int W = decltype(which)::value, REQUEST = decltype(request)::value;
     constexpr int kAll = kRowsHalf * S::NT;
+    constexpr int kFrom = REQUEST == 1 ? kHalf : 0, kCount = REQUEST == 1 ? S::kLoads - kHalf : kHalf;
     __builtin_amdgcn_sched_barrier(0);
     if (on) {
 #pragma unroll
@@ -327,16 +348,16 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
           const int n = i * S::NT + j;
           if constexpr (REQUEST >= 0) {
 #pragma unroll
-            for (int l = n * kHalf / kAll; l < (n + 1) * kHalf / kAll; ++l) {
+            for (int l = n * kCount / kAll; l < (n + 1) * kCount / kAll; ++l) {
               __builtin_amdgcn_sched_barrier(0);
-              load(REQUEST * kHalf + l);
+              load(kFrom + l);
               __builtin_amdgcn_sched_barrier(0);
             }
           }
         }
     } else if constexpr (REQUEST >= 0) {
 #pragma unroll
-      for (int l = 0; l < kHalf; ++l) load(REQUEST * kHalf + l);
+      for (int l = 0; l < kCount; ++l) load(kFrom + l);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -359,7 +380,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
 #pragma unroll
       for (int i = 0; i < S::MT; ++i) acc[j][i] = f32x4{};
     if constexpr (P == Product::kWeights) {
-      if (!p.accumulate || t.depth == 0) return;
+      if (!p.accumulate || t.depth == 0 || part > 0) return;
 #pragma unroll
       for (int i = 0; i < S::MT; ++i) {
         const int row = t.i0 + (wm * S::MT + i) * 16 + col;
@@ -405,6 +426,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
           else
             *reinterpret_cast<dwords2*>(to + (at & 8)) = pack4<TO>(v);
         }
+        asm volatile("" ::: "memory");  // other lanes read what this one wrote
         const int in = lane % kSlots * (16 / kBytes<TO>);
         const int j = t.j0 + wn * S::NT * 16 + c0 + in;
 #pragma unroll
@@ -425,7 +447,30 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
                     kBytes<TO> == 4 ? d[x % 4] : d[x / 2] >> (16 * (x & 1)));
           }
         }
+        asm volatile("" ::: "memory");
       }
+    }
+  };
+  // The groups' sums, added in halves until the first group holds them.
+  auto join = [&]() {
+#pragma unroll
+    for (int h = S::KS / 2; h > 0; h >>= 1) {
+      auto* at = reinterpret_cast<f32x4*>(sums) +
+                 ((part % h) * S::kGroup + in_group) * S::MT * S::NT * 64 + lane;
+      if (part >= h && part < 2 * h) {
+#pragma unroll
+        for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+          for (int i = 0; i < S::MT; ++i) at[(j * S::MT + i) * 64] = acc[j][i];
+      }
+      wait_lds_and_barrier();
+      if (part < h) {
+#pragma unroll
+        for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+          for (int i = 0; i < S::MT; ++i) acc[j][i] += at[(j * S::MT + i) * 64];
+      }
+      wait_lds_and_barrier();
     }
   };
 
@@ -442,12 +487,13 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   Tile t = locate(0);
   int chunks = chunks_of(t);
   begin(t);
-  Columns y = read_columns(ring, 0), y1;
-  Rows x = read_rows(ring, 0, 0), x1;
+  Columns y = read_columns(ring + part * S::kPart, 0), y1;
+  Rows x = read_rows(ring + part * S::kPart, 0, 0), x1;
   bool first = has_rows(t, 0), second = has_rows(t, 1);
   for (int n = 0, c = 0;;) {
-    const bool more = P == Product::kWeights || t.depth - c * kChunk > kChunk / 2;
-    const uint8_t* st = ring + stage;
+    const bool more =
+        P == Product::kWeights || t.depth - c * S::kDepth - part * kChunk > kChunk / 2;
+    const uint8_t* st = ring + stage + part * S::kPart;
     x1 = read_rows(st, 0, 1);
     multiply(x, y, kFirst, kSecond, first);
     move_on();
@@ -462,16 +508,17 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
     wait_loads_and_barrier<(S::STAGES - 2) * S::kLoads>();
     stage = stage + S::kStage == S::STAGES * S::kStage ? 0 : stage + S::kStage;
     prepare();
-    y = read_columns(ring + stage, 0);
-    x = read_rows(ring + stage, 0, 0);
+    y = read_columns(ring + stage + part * S::kPart, 0);
+    x = read_rows(ring + stage + part * S::kPart, 0, 0);
     multiply(x1, y1, kSecond, kFirst, second && more);
     if (++c < chunks) continue;
-    if (P == Product::kWeights && p.accumulate && t.depth == 0) {
-      // stays as it is
+    if constexpr (S::KS > 1) join();
+    if (part > 0 || (P == Product::kWeights && p.accumulate && t.depth == 0)) {
+      // nothing to store, or what is there stays
     } else if (t.i1 - t.i0 == S::BM && t.j0 + S::BN <= cols) {
-      store(t, turn + wave * S::kScratch, std::true_type{});
+      store(t, turn + in_group * S::kScratch, std::true_type{});
     } else {
-      store(t, turn + wave * S::kScratch, std::false_type{});
+      store(t, turn + in_group * S::kScratch, std::false_type{});
     }
     if (++n == mine) break;
     t = locate(n);
@@ -504,9 +551,11 @@ void launch_grouped_tiles(const GroupedArgs& a, hipStream_t stream) {
   args.col_tiles = (cols + S::BN - 1) / S::BN;
   args.by_expert = Divisor(args.row_tiles * args.col_tiles);
   args.by_group = Divisor(kGroupTiles * args.col_tiles);
+  args.parts = a.parts > 1 ? a.parts : 1;
+  args.by_parts = Divisor(args.parts);
   // at most one short tile per expert; no more workgroups than run at once
   const int64_t row_tiles =
-      P == Product::kWeights ? static_cast<int64_t>(a.E) * args.row_tiles
+      P == Product::kWeights ? static_cast<int64_t>(a.E) * args.parts * args.row_tiles
                              : a.rows / S::BM + (a.E < a.rows ? a.E : a.rows);
   const int64_t resident = static_cast<int64_t>(device_info().cus) * S::per_cu(P);
   static_assert(S::per_cu(P) >= 1, "the ring fits in LDS");
@@ -520,5 +569,41 @@ void launch_grouped_tiles(const GroupedArgs& a, hipStream_t stream) {
 
 using Grouped256 = GroupedShape<256, 256, 2, 4, 2>;
 using Grouped128 = GroupedShape<128, 128, 2, 2, 2>;
+using Grouped64 = GroupedShape<64, 64, 2, 2, 4>;
+using GroupedSplit = GroupedShape<32, 32, 1, 1, 2, 8>;
+
+// What a product takes per chunk of the reduction with `tiles` tiles of a shape, in units of
+// 10 ns: the time of a chunk where the tiles fill the compute units once, as often as they do.
+//   256 x 256, one on a unit   1.5 us (8192 cubed: 512 chunks 790 us)
+//   128 x 128, one             0.65 us (2048 cubed, 256 tiles, 32 chunks: 26 us)
+//              two             1.0 us (2048 x 4096 x 4096, 512 tiles, 64 chunks: 64 us)
+//   64 x 64,   one, two        0.37, 0.47 us (1000 x 1024 x 1024, 256 tiles, 16 chunks: 9.4 us;
+//                              400 x 4096 x 4096, 448 tiles, 64 chunks: 31 us)
+//              more            0.6 us a turn of two (2048 cubed, 1024 tiles: 33 us)
+constexpr int64_t kUnits = 256;  // compute units of the chip that the rules go by
+inline int64_t cost_of(int size, int64_t tiles) {
+  const int64_t pairs = (tiles + 2 * kUnits - 1) / (2 * kUnits);
+  if (size == 256) return 150 * ((tiles + kUnits - 1) / kUnits);
+  if (size == 128) return tiles <= kUnits ? 65 : 100 * pairs;
+  return tiles <= kUnits ? 37 : pairs <= 1 ? 47 : 60 * pairs;
+}
+
+// The tile's size of the least cost, of two equal ones the larger; tiles(size) counts.
+template <typename F>
+int pick_size(F&& tiles) {
+  int best = 256;
+  for (int size : {128, 64})
+    if (cost_of(size, tiles(size)) < cost_of(best, tiles(best))) best = size;
+  return best;
+}
+
+// Tiles of a product of rows: experts that hold `mean` rows each, more or less, so that their
+// last tile is half full.
+inline int64_t row_product_tiles(int64_t active, int64_t mean, int cols, int size) {
+  const int64_t col_tiles = (cols + size - 1) / size;
+  if (active == 1) return (mean + size - 1) / size * col_tiles;
+  const int64_t all = active * col_tiles, tiles = all * (2 * mean + size) / (2 * size);
+  return tiles > all ? tiles : all;
+}
 
 }  // namespace moe

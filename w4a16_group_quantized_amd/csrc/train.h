@@ -46,7 +46,8 @@ struct GroupedArgs {
   float* partial;     // kWeights: workspace of grouped_workspace_bytes
   // set at the launch
   int row_tiles, col_tiles;  // row_tiles: of an expert, kWeights only
-  Divisor by_expert, by_group;
+  int parts;                 // kWeights: shares of an expert's rows, each a sum of its own
+  Divisor by_expert, by_group, by_parts;
 };
 size_t grouped_workspace_bytes(int64_t rows, int E, int N, int K);
 // With tiles of 16-byte loads (grouped_out.hip, grouped_rows.hip, grouped_weights.hip).
