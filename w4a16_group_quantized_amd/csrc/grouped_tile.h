@@ -407,6 +407,11 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
     constexpr int kWide = kCols < S::NT * 16 ? kCols : S::NT * 16;
     static_assert(S::NT * 16 % kWide == 0, "columns turn evenly");
     auto slot = [](int row, int n) { return (n ^ row) & (kSlots - 1); };
+    // addresses are worked out here, not once for all tiles: they would hold registers
+    // through the main loop
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const int col = lane & 15, g = lane >> 4;
     const int64_t out_ld = P == Product::kWeights ? p.K : p.out_ld;
     auto* out = static_cast<typename TO::bits*>(p.out) +
                 (P == Product::kWeights ? static_cast<int64_t>(t.e) * p.N * p.K : 0);
