@@ -12,51 +12,68 @@ namespace moe {
 namespace {
 
 // ------------------------------------------------------------- any alignment --
-// Sizes, strides and addresses that the tile kernels' 16-byte loads do not take:
-// a workgroup of four waves makes a tile of 64 x 64, 32 of the reduction at a
-// time through registers into LDS, element by element at ragged ends.
-constexpr int kAnyTile = 64, kAnyDepth = 32, kAnyRow = kAnyDepth + 8;
+// Sizes, strides and addresses that the tile kernels' 16-byte loads do not take: a
+// workgroup of four waves makes a tile of 64 x 64, 32 of the reduction at a time
+// through registers into LDS, element by element at ragged ends.  As in the tile
+// kernels an operand stays as it lies in memory, and one whose reduction runs across
+// the rows is read through the transposing load (turned at its store into LDS, element
+// by element, the gradients below took 5.3 and 8.2 ms).  8 experts of 8191 x 4096,
+// 16381 rows: 3.1 ms, gradients 2.9 and 2.6, a third of the tile kernels' rate: nothing
+// is on its way while a tile is multiplied.
+constexpr int kAnyTile = 64, kAnyDepth = 32;
+constexpr int kAnyAlong = kAnyDepth + 8, kAnyAcross = kAnyTile + 8;  // a row's elements in LDS
+constexpr int kAnyElements = kAnyTile * kAnyAlong;
+static_assert(kAnyDepth * kAnyAcross <= kAnyElements, "either layout fits");
 
 // An operand seen as [i, q], q along the reduction: one of its two strides is 1.
+template <bool ALONG>  // q is the contiguous one
 struct View {
   const uint16_t* base;
   int64_t ld;      // the other stride
-  bool along;      // q is the contiguous one
   int n, depth;    // i < n, q < depth
-};
 
-__device__ __forceinline__ void any_load(const View& v, int i0, int q0,
-                                         uint16_t (*tile)[kAnyRow]) {
-  const int u = threadIdx.x;
-  uint16_t e[8];
-  const int i = i0 + (v.along ? u >> 2 : (u & 7) * 8), q = q0 + (v.along ? (u & 3) * 8 : u >> 3);
-  const bool in = i < v.n && q < v.depth;
-  const uint16_t* p = v.base + (v.along ? i * v.ld + q : q * v.ld + i);
-  const int left = in ? (v.along ? v.depth - q : v.n - i) : 0;
-  if (left >= 8) {
-    const dwords4 d = load16(p);
+  __device__ __forceinline__ void load(int i0, int q0, uint16_t* tile) const {
+    const int u = threadIdx.x;
+    const int r = ALONG ? u >> 2 : u >> 3, c = (ALONG ? u & 3 : u & 7) * 8;
+    const int i = i0 + (ALONG ? r : c), q = q0 + (ALONG ? c : r);
+    const bool in = i < n && q < depth;
+    const uint16_t* p = base + (ALONG ? i * ld + q : q * ld + i);
+    const int left = in ? (ALONG ? depth - q : n - i) : 0;
+    dwords4 d{};
+    if (left >= 8) {
+      d = load16(p);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = static_cast<uint16_t>(d[j / 2] >> (16 * (j & 1)));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = j < left ? p[j] : uint16_t{0};
+      for (int j = 0; j < 8; ++j)
+        d[j / 2] |= j < left ? static_cast<uint32_t>(p[j]) << (16 * (j & 1)) : 0u;
+    }
+    *reinterpret_cast<dwords4*>(tile + r * (ALONG ? kAnyAlong : kAnyAcross) + c) = d;
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (v.along)
-      tile[u >> 2][(u & 3) * 8 + j] = e[j];
-    else
-      tile[(u & 7) * 8 + j][u >> 3] = e[j];
+  // The fragment of 16 i from `first` on: this lane's i and 8 q.
+  static __device__ __forceinline__ dwords4 read(const uint16_t* tile, int first) {
+    const int l = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
+    if constexpr (ALONG) {
+      return *reinterpret_cast<const dwords4*>(tile + (first + l) * kAnyAlong + 8 * g);
+    } else {
+      typedef short v4i16 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) v4i16* LdsPtr;
+      const uint16_t* p = tile + (8 * g + (l >> 2)) * kAnyAcross + first + (l & 3) * 4;
+      const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p));
+      const auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p + 4 * kAnyAcross));
+      const dwords2 a = __builtin_bit_cast(dwords2, lo), b = __builtin_bit_cast(dwords2, hi);
+      return dwords4{a[0], a[1], b[0], b[1]};
+    }
   }
-}
+};
 
 template <Product P, typename T, typename TO>
 __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedArgs p, int col_tiles) {
-  __shared__ __attribute__((aligned(16))) uint16_t xs[kAnyTile][kAnyRow], ys[kAnyTile][kAnyRow];
+  __shared__ __attribute__((aligned(16))) uint16_t xs[kAnyElements], ys[kAnyElements];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int cols = P == Product::kOut ? p.N : p.K;
   int e, i0, i1, j0 = 0;
-  View x, y;
+  View<P != Product::kWeights> x;
+  View<P == Product::kOut> y;
   if constexpr (P == Product::kWeights) {
     const int row_tiles = (p.N + kAnyTile - 1) / kAnyTile;
     const int per = row_tiles * col_tiles;
@@ -68,28 +85,27 @@ __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedArgs p, int col
     int r0, r1;
     segment(p, e, r0, r1);
     const int n = max(r1 - r0, 0);
-    x = View{p.x + r0 * p.x_ld, p.x_ld, false, p.N, n};
-    y = View{p.y + r0 * p.y_ld, p.y_ld, false, p.K, n};
+    x = {p.x + r0 * p.x_ld, p.x_ld, p.N, n};
+    y = {p.y + r0 * p.y_ld, p.y_ld, p.K, n};
   } else {
     const int mt = blockIdx.x / col_tiles;
     j0 = (blockIdx.x - mt * col_tiles) * kAnyTile;
     if (!find_tile(count_tiles(p.offsets, p.E, p.rows, kAnyTile), mt, e, i0, i1)) return;
     const uint16_t* w = p.y + static_cast<int64_t>(e) * p.N * p.K;
     const int depth = P == Product::kOut ? p.K : p.N;
-    x = View{p.x, p.x_ld, true, i1, depth};
-    y = View{w, p.K, P == Product::kOut, cols, depth};
+    x = {p.x, p.x_ld, i1, depth};
+    y = {w, p.K, cols, depth};
   }
   // wave w makes columns 16 w ... + 15 of all 64 rows
   const int col = lane & 15, g = lane >> 4;
   f32x4 acc[4] = {};
   for (int q = 0; q < x.depth; q += kAnyDepth) {
-    any_load(x, i0, q, xs);
-    any_load(y, j0, q, ys);
+    x.load(i0, q, xs);
+    y.load(j0, q, ys);
     __syncthreads();
-    const dwords4 a = *reinterpret_cast<const dwords4*>(&ys[wave * 16 + col][8 * g]);
+    const dwords4 a = y.read(ys, wave * 16);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      acc[i] = mfma16(T{}, a, *reinterpret_cast<const dwords4*>(&xs[i * 16 + col][8 * g]), acc[i]);
+    for (int i = 0; i < 4; ++i) acc[i] = mfma16(T{}, a, x.read(xs, i * 16), acc[i]);
     __syncthreads();
   }
   const int j = j0 + wave * 16 + 4 * g;

@@ -18,6 +18,22 @@
 // be replaced stands before the last half step's products, whose fragments are in
 // registers by then, and behind it the next chunk's first fragments are read.  A wave
 // so has products to issue on both sides of the one barrier of a chunk.
+//
+// 8192 cubed, 256 x 256 tiles, bf16: 780 us (1.41 PFLOP/s), its gradients 762 and 754.
+// The matrix units are busy 70 % of the cycles there and the clock falls to 1.9 GHz of
+// 2.4, so it is the power as much as the cycles that bounds it: the same loop took 9 %
+// fewer cycles after its scalar steps were cut and 1 % less time; 32 x 32 matrix
+// instructions, which move twice the sums, took 855 us; with all loads of a chunk hitting
+// one chunk in L2 741.  Measured slower: the next chunk's loads all behind the barrier
+// (weights 754 -> 815 us) or over three half steps (770); three or four stages of smaller
+// tiles; four waves of 128 x 128 with the sums in accumulation registers (13 % more cycles:
+// a lone wave of a SIMD has nothing to issue while its loads are taken).
+// 512 experts of 1280 x 2560, 40960 rows, 128 x 128 tiles: 700 us (5.2 TB/s), gradient of
+// the rows 764 (4.8): bound by reading the weights.  Gradient of the weights, 840 us (4.4
+// TB/s): bound by writing it, and by its two chunks a tile, which wait for the stores of
+// the tile before since loads and stores are counted in one order; with 10240 rows, one
+// chunk, 602 us (5.7 TB/s).  Nontemporal stores there: plain ones 878 us, and 569 for 385
+// of 512 experts of 2560 x 640.
 #pragma once
 
 #include "tiles.h"
@@ -406,7 +422,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
     constexpr int kCols = S::kTurn / kBytes<TO>, kSlots = S::kTurn / 16, kRows = 64 / kSlots;
     constexpr int kWide = kCols < S::NT * 16 ? kCols : S::NT * 16;
     static_assert(S::NT * 16 % kWide == 0, "columns turn evenly");
-    auto slot = [](int row, int n) { return (n ^ row) & (kSlots - 1); };
+    auto slot = [](int row, int n) { return (n ^ (row >> 1)) & (kSlots - 1); };
     // addresses are worked out here, not once for all tiles: they would hold registers
     // through the main loop
     int lane = threadIdx.x & 63;

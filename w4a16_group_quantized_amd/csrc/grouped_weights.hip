@@ -9,8 +9,8 @@ int64_t tiles_of(int64_t blocks, int N, int K, int size) {
 }
 
 // Tiles of 256 where they do not hang over the matrix by more than an eighth: 128 experts
-// of 1280 x 640, 8000 rows, 50 us, with tiles of 128 x 128 42; 512 of 1280 x 2560, 40960
-// rows, 827 and 1194.
+// of 1280 x 640, 8000 rows, 50 us, with tiles of 128 x 128 46; 512 of 1280 x 2560, 40960
+// rows, 840 and 1076; 8 of 8192 x 4096, 16381 rows, 861 and 1073.
 int size_of(int64_t blocks, int N, int K) {
   const bool fits = tiles_of(1, N, K, 256) * 65536 <= static_cast<int64_t>(N) * K / 8 * 9;
   const auto tiles = [&](int size) { return tiles_of(blocks, N, K, size); };

