@@ -281,7 +281,14 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
       sy.aim(p.y + t.e * w + skip, (w - skip) * 2, false);
     }
   };
+  // The tile that is requested now, and the one before it.  With two stages the tile that
+  // is multiplied next is one of them: it need not be located again.
   int load_tile = 0;
+  Tile ahead = locate(0), held = ahead;
+  auto tile_of = [&](int n) {
+    if constexpr (S::STAGES > 2) return locate(n);
+    return load_tile == n ? ahead : held;
+  };
   const uint32_t ring_at = lds_address(ring);
   uint32_t load_at = ring_at;
   // Half of the next chunk's loads are requested at a time; the second half moves on,
@@ -309,8 +316,10 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
         sy.range.d[2] = tail_y;
       }
     } else if (++load_tile < mine) {
-      aim(locate(load_tile));
+      held = ahead;
+      aim(ahead = locate(load_tile));
     } else {
+      held = ahead;
       sx.stop();
       sy.stop();
       load_left = INT32_MAX;
@@ -431,6 +440,9 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
     const int64_t out_ld = P == Product::kWeights ? p.K : p.out_ld;
     auto* out = static_cast<typename TO::bits*>(p.out) +
                 (P == Product::kWeights ? static_cast<int64_t>(t.e) * p.N * p.K : 0);
+    // where this lane stores, from the first of 16 rows and kWide columns on
+    const int in = lane % kSlots * (16 / kBytes<TO>);
+    const int64_t lane_at = lane / kSlots * out_ld + in;
 #pragma unroll
     for (int i = 0; i < S::MT; ++i) {
       const int row0 = t.i0 + (wm * S::MT + i) * 16;
@@ -448,8 +460,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
             *reinterpret_cast<dwords2*>(to + (at & 8)) = pack4<TO>(v);
         }
         asm volatile("" ::: "memory");  // other lanes read what this one wrote
-        const int in = lane % kSlots * (16 / kBytes<TO>);
-        const int j = t.j0 + wn * S::NT * 16 + c0 + in;
+        const int j0 = t.j0 + wn * S::NT * 16 + c0;
 #pragma unroll
         for (int r = 0; r < 16; r += kRows) {
           const int row = r + lane / kSlots;
@@ -457,13 +468,13 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
               *reinterpret_cast<const dwords4*>(place + row * S::kTurn + slot(row, lane) * 16);
           if (kWide < kCols && in >= kWide) continue;
           if (!WHOLE && row0 + row >= t.i1) continue;
-          auto* o = out + (row0 + row) * out_ld + j;
-          if (WHOLE || j + 16 / kBytes<TO> <= cols) {
+          auto* o = out + ((row0 + r) * out_ld + j0) + lane_at;
+          if (WHOLE || j0 + in + 16 / kBytes<TO> <= cols) {
             store16(o, d);
           } else {
 #pragma unroll
             for (int x = 0; x < 16 / kBytes<TO>; ++x)
-              if (j + x < cols)
+              if (j0 + in + x < cols)
                 o[x] = static_cast<typename TO::bits>(
                     kBytes<TO> == 4 ? d[x % 4] : d[x / 2] >> (16 * (x & 1)));
           }
@@ -495,7 +506,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
     }
   };
 
-  aim(locate(0));
+  aim(ahead);
 #pragma unroll
   for (int s = 0; s < S::STAGES; ++s) {
     prepare();
@@ -505,7 +516,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   }
   wait_loads_and_barrier<(S::STAGES - 2) * S::kLoads + kHalf>();
   uint32_t stage = 0;
-  Tile t = locate(0);
+  Tile t = tile_of(0);
   int chunks = chunks_of(t);
   begin(t);
   Columns y = read_columns(ring + part * S::kPart, 0), y1;
@@ -542,7 +553,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
       store(t, turn + in_group * S::kScratch, std::false_type{});
     }
     if (++n == mine) break;
-    t = locate(n);
+    t = tile_of(n);
     chunks = chunks_of(t);
     c = 0;
     first = has_rows(t, 0);

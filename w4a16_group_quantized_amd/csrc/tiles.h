@@ -145,15 +145,21 @@ __device__ __forceinline__ bool find_tile(const Tiles& t, int mt, int& e, int& r
 
 typedef uint32_t dwords2 __attribute__((ext_vector_type(2)));
 
+// Two values rounded to nearest even, in one word, low half first: one instruction for
+// both.
+__device__ __forceinline__ uint32_t pack2(F16, float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, h2_t));
+}
+__device__ __forceinline__ uint32_t pack2(BF16, float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, b2_t));
+}
 // Four results of a 16-bit type, rounded, in two words.
 template <typename T>
 __device__ __forceinline__ dwords2 pack4(f32x4 v) {
-  dwords2 d;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    d[i] = static_cast<uint32_t>(from_float(T{}, v[2 * i])) |
-           (static_cast<uint32_t>(from_float(T{}, v[2 * i + 1])) << 16);
-  return d;
+  return dwords2{pack2(T{}, v[0], v[1]), pack2(T{}, v[2], v[3])};
 }
 
 template <typename T>
