@@ -25,15 +25,14 @@
 // fewer cycles after its scalar steps were cut and 1 % less time; 32 x 32 matrix
 // instructions, which move twice the sums, took 855 us; with all loads of a chunk hitting
 // one chunk in L2 741.  Measured slower: the next chunk's loads all behind the barrier
-// (weights 754 -> 815 us) or over three half steps (770); three or four stages of smaller
-// tiles; four waves of 128 x 128 with the sums in accumulation registers (13 % more cycles:
-// a lone wave of a SIMD has nothing to issue while its loads are taken).
+// (weights 754 -> 815 us) or over three half steps (770), and three or four stages of
+// smaller tiles.
 // 512 experts of 1280 x 2560, 40960 rows, 128 x 128 tiles: 700 us (5.2 TB/s), gradient of
-// the rows 764 (4.8): bound by reading the weights.  Gradient of the weights, 840 us (4.4
-// TB/s): bound by writing it, and by its two chunks a tile, which wait for the stores of
-// the tile before since loads and stores are counted in one order; with 10240 rows, one
-// chunk, 602 us (5.7 TB/s).  Nontemporal stores there: plain ones 878 us, and 569 for 385
-// of 512 experts of 2560 x 640.
+// the rows 770 (4.8): bound by reading the weights.  Gradient of the weights, 810 us (4.5
+// TB/s): bound by writing it and by the two chunks of a tile, which add to the stores (with
+// 10240 rows, one chunk, 590 us, 5.8 TB/s).  Waiting for a tile's stores later than at the
+// next barrier gave nothing (840 -> 863 us).  Stores are nontemporal: with plain ones 878
+// us against 840, and 569 against 385 at 2560 x 640.
 #pragma once
 
 #include "tiles.h"
