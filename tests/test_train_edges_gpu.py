@@ -248,3 +248,19 @@ def test_captured_adamw(ops):
             step(b, sb)
             torch.cuda.synchronize()
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# ---- narrow matrices -------------------------------------------------------------------
+@pytest.mark.parametrize("counts,N,K", [([65], 8, 8), ([129, 65, 1, 193], 24, 16), ([70, 0, 130], 1024, 8),
+                                        ([66] * 300, 8, 512)])
+def test_weight_gradient_of_rows_shorter_than_a_tile(ops, counts, N, K):
+    """The last segment ends with the tensors and with a few rows in its last chunk: what the rows before
+    them read past their ends must stay inside.  Rows of other segments do not get in either."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    R = sum(counts)
+    grad, a = (torch.randn((R, n), generator=g, device="cuda").to(BF16) for n in (N, K))
+    off = torch.tensor([0, *np.cumsum(counts)], dtype=torch.int32, device="cuda")
+    got = np64(ops.moe_grouped_gemm_backward_weights(grad, a, off, dtype=F32))
+    seg, g_h, a_h = off.cpu().numpy(), np64(grad), np64(a)
+    size = ref.product_weights(abs(g_h), abs(a_h), seg)
+    assert (abs(got - ref.product_weights(g_h, a_h, seg)) <= (max(counts) + 1) * 2.0 ** -23 * size).all()

@@ -261,17 +261,20 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   sx.init(in_group, part, p.x_ld);
   sy.init(in_group, part, P == Product::kWeights ? p.y_ld : p.K);
   int load_left = 0;  // of the reduction
-  uint32_t tail_x = 0, tail_y = 0;  // kWeights: bytes that hold the last chunk's rows
+  uint32_t tail_x = 0, tail_y = 0;  // kWeights: bytes from the last chunk to the rows' end
   auto aim = [&](const Tile& t) {
     load_left = t.depth;
     if constexpr (P == Product::kWeights) {
-      // Rows of the segment, each from the tile's first column to the matrix's last.  All
-      // stages but the last have all their rows, whatever a row's end reads of the next.
+      // Rows of the segment, each from the tile's first column to the matrix's last.  What a
+      // chunk's last row reads behind its end is the next chunk's, up to BM / 8 rows of it: the
+      // range is open until two chunks are left.
+      static_assert(S::BM / 8 <= S::kDepth && S::BN / 8 <= S::kDepth, "no further than a chunk");
       const int64_t n = (t.depth - 1) % S::kDepth;
       tail_x = t.depth > 0 ? static_cast<uint32_t>((n * p.x_ld + p.N - t.i0) * 2) : 0;
       tail_y = t.depth > 0 ? static_cast<uint32_t>((n * p.y_ld + p.K - t.j0) * 2) : 0;
-      sx.aim(p.x + t.r0 * p.x_ld + t.i0, t.depth > S::kDepth ? INT32_MAX : tail_x, true);
-      sy.aim(p.y + t.r0 * p.y_ld + t.j0, t.depth > S::kDepth ? INT32_MAX : tail_y, true);
+      const bool open = t.depth > 2 * S::kDepth, two = t.depth > S::kDepth;
+      sx.aim(p.x + t.r0 * p.x_ld + t.i0, open ? INT32_MAX : tail_x + (two ? sx.step : 0), true);
+      sy.aim(p.y + t.r0 * p.y_ld + t.j0, open ? INT32_MAX : tail_y + (two ? sy.step : 0), true);
     } else {
       const int64_t w = static_cast<int64_t>(p.N) * p.K;
       const int64_t skip = P == Product::kOut ? static_cast<int64_t>(t.j0) * p.K : t.j0;
@@ -310,9 +313,10 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
     if (load_left > 0) {
       sx.move_on();
       sy.move_on();
-      if (P == Product::kWeights && load_left <= S::kDepth) {
-        sx.range.d[2] = tail_x;
-        sy.range.d[2] = tail_y;
+      if (P == Product::kWeights && load_left <= 2 * S::kDepth) {
+        const bool two = load_left > S::kDepth;
+        sx.range.d[2] = tail_x + (two ? sx.step : 0);
+        sy.range.d[2] = tail_y + (two ? sy.step : 0);
       }
     } else if (++load_tile < mine) {
       held = ahead;
