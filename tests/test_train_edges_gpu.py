@@ -264,3 +264,20 @@ def test_weight_gradient_of_rows_shorter_than_a_tile(ops, counts, N, K):
     seg, g_h, a_h = off.cpu().numpy(), np64(grad), np64(a)
     size = ref.product_weights(abs(g_h), abs(a_h), seg)
     assert (abs(got - ref.product_weights(g_h, a_h, seg)) <= (max(counts) + 1) * 2.0 ** -23 * size).all()
+
+
+# ---- AdamW without eps --------------------------------------------------------------------
+@pytest.mark.parametrize("eps", [0.0, 1e-21])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_of_subnormal_second_moments(ops, bits, eps):
+    """Gradients of 1e-20 to 1e-16 square to fp32's subnormal numbers: the step is lr all the same."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    n = 1000
+    grad = 10.0 ** -(16 + 4 * torch.rand(n, generator=g, device="cuda")) * torch.randn(n, generator=g, device="cuda").sign()
+    p = torch.ones(n, device="cuda")
+    m, v = ops.adamw_states(p, bits)
+    ops.moe_adamw([p], [grad], [m], [v], lr=1e-2, beta1=0.9, beta2=0.999, eps=eps, weight_decay=0.0, step=1)
+    x = grad.cpu().numpy()
+    m32, v32 = np.float32(1 - 0.9) * x, np.float32(1 - 0.999) * (x * x)  # in fp32, as the kernel's
+    step = 1e-2 * (m32.astype(np.float64) / 0.1) / (np.sqrt(v32.astype(np.float64) / 0.001) + eps)
+    assert (abs(np64(p) - (1 - step)) <= 2e-5 * abs(step) + 2.0 ** -23).all()

@@ -241,6 +241,7 @@ int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, int32_t state_bits
   s.eps = static_cast<float>(eps);
   s.grad_scale = grad_scale;
   s.seed = seed;
+  s.small = ldexp(static_cast<double>(s.root), -63) > ldexp(static_cast<double>(s.eps), -25);
   launch_adamw(tensors, count, state_bits, s, static_cast<hipStream_t>(stream));
   return check_launch();
 }

@@ -186,10 +186,21 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Batch b, AdamwScalars s
       v[i] = s.beta2 * v[i] + s.rest2 * (gi * gi);
     }
   }
+  float root[8];
+  if (s.small) {  // the root's instruction takes v under 2^-126 for 0
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool tiny = v[i] < 0x1p-96f;
+      root[i] = __builtin_amdgcn_sqrtf(v[i] * (tiny ? 0x1p64f : 1.f)) * (tiny ? 0x1p-32f : 1.f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) root[i] = __builtin_amdgcn_sqrtf(v[i]);
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float root = fmaf(__builtin_amdgcn_sqrtf(v[i]), s.root, s.eps);
-    p[i] = fmaf(-s.size, m[i] * __builtin_amdgcn_rcpf(root), p[i] * s.keep);
+    const float over = fmaf(root[i], s.root, s.eps);
+    p[i] = fmaf(-s.size, m[i] * __builtin_amdgcn_rcpf(over), p[i] * s.keep);
   }
   if constexpr (BITS == 8) {
     uint32_t noise[8], more[8];
