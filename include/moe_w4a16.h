@@ -766,9 +766,8 @@ int moe_combine_backward(const void* grad_out, int32_t grad_dtype,
  *                   contents on entry are ignored.  Two calls that overlap in
  *                   time must not share it.
  *
- * Any N, K, strides and element-aligned addresses; where N, K, the strides and
- * the addresses are multiples of 8 elements the calls are several times as
- * fast.  An output must not overlap an input.  rows == 0 is valid;
+ * Any N, K and strides; where N, K, the strides and the addresses of a and grad
+ * are multiples of 8 elements the calls are several times as fast.  An output must not overlap an input.  rows == 0 is valid;
  * moe_grouped_gemm_backward_weights then still writes grad_w.
  *
  * Limits: fp32 operands are MOE_ERR_UNSUPPORTED; 1 <= E <= 4096; 1 <= N, K <=
@@ -831,9 +830,9 @@ int moe_silu_mul_backward(const void* grad_act, int64_t grad_stride,
  *   topk_ids      in   int32 [T, top_k]
  *   topk_weights  in   fp32 [T, top_k]
  *   grad_weights  in   fp32 [T, top_k]
- *   grad_logits   out  out_dtype [T, E]
+ *   grad_logits   out  out_dtype [T, E]; must not overlap an input
  *
- * Limits: 1 <= E <= 4096; 1 <= top_k <= 64; T * top_k < 2^31.
+ * Limits: 1 <= E <= 4096; 1 <= top_k <= 64; T < 2^26; T * top_k < 2^31.
  */
 int moe_route_backward(const int32_t* topk_ids, const float* topk_weights,
                        const float* grad_weights, int64_t T, int32_t E,
@@ -847,7 +846,8 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_weights,
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
  * in fp32; p is rounded once to its type (and once to copy's), and is updated
- * from m and v before these are rounded to their states.
+ * from m and v before these are rounded to their states.  With eps 0 an element
+ * whose v is 0 divides by 0.
  *
  * States of 8 bits: elements in blocks of MOE_ADAMW_BLOCK (the last may be
  * short), per block one fp32 scale = largest magnitude / 1.875.  A code's

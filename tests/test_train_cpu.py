@@ -251,3 +251,9 @@ def test_oracle_adamw_first_step():
     g = np.array([0.5, -2.0, 1e-3])
     p, m, v = ref.adamw(np.zeros(3), g, np.zeros(3), np.zeros(3), 0.1, 0.9, 0.999, 0.0, 0.0, 1)
     assert np.allclose(p, -0.1 * np.sign(g)) and np.allclose(m, 0.1 * g) and np.allclose(v, 1e-3 * g * g)
+
+
+# ---- limits of a launch, and tensors given twice ------------------------------------------
+@pytest.mark.parametrize("T", [1 << 26, (1 << 31) - 1])
+def test_route_backward_of_more_tokens_than_a_launch_takes(T):
+    assert ops.load_library().moe_route_backward(FAKE, FAKE, FAKE, T, 8, 1, FAKE, 0, None) == UNSUPPORTED

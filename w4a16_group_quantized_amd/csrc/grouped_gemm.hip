@@ -75,10 +75,8 @@ __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedArgs p, int col
   View<P != Product::kWeights> x;
   View<P == Product::kOut> y;
   if constexpr (P == Product::kWeights) {
-    const int row_tiles = (p.N + kAnyTile - 1) / kAnyTile;
-    const int per = row_tiles * col_tiles;
-    e = blockIdx.x / per;
-    const int at = blockIdx.x - e * per;
+    const int at = blockIdx.x;
+    e = blockIdx.y;
     i0 = at / col_tiles * kAnyTile;
     i1 = min(p.N, i0 + kAnyTile);
     j0 = at % col_tiles * kAnyTile;
@@ -133,10 +131,10 @@ template <Product P>
 void launch_any(const GroupedArgs& a, hipStream_t stream) {
   const int cols = P == Product::kOut ? a.N : a.K;
   const int col_tiles = (cols + kAnyTile - 1) / kAnyTile;
-  const int64_t row_tiles =
-      P == Product::kWeights ? static_cast<int64_t>(a.E) * ((a.N + kAnyTile - 1) / kAnyTile)
-                             : a.rows / kAnyTile + (a.E < a.rows ? a.E : a.rows);
-  const dim3 grid(static_cast<unsigned>(row_tiles * col_tiles));
+  const int64_t row_tiles = P == Product::kWeights ? (a.N + kAnyTile - 1) / kAnyTile
+                                                   : a.rows / kAnyTile + (a.E < a.rows ? a.E : a.rows);
+  // an expert's tiles along x, for which a launch's 2^32 threads are enough
+  const dim3 grid(static_cast<unsigned>(row_tiles * col_tiles), P == Product::kWeights ? a.E : 1);
   with_types(a, [&](auto t, auto to) {
     hipLaunchKernelGGL((grouped_any_kernel<P, decltype(t), decltype(to)>), grid, dim3(256), 0,
                        stream, a, col_tiles);

@@ -19,7 +19,8 @@ constexpr int kThreads = 256;
 // 1 / (1 + z) and z / (1 + z) in one order or the other.  The exponential is that of
 // 2^t (1 + r ln 2) with t = -|x| log2(e) rounded and r what that rounding left (2
 // units in the last place); |x| is held below 128, where z is 0 already, so that r
-// stays finite.  A NaN goes through the caller's products with x.
+// stays finite.  A z under 2^-126 counts as 0.  A NaN goes through the caller's
+// products with x.
 __device__ __forceinline__ void sigmoid(float x, float& s, float& rest) {
   constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f, kLn2 = 0.693147181f;
   const float a = -fminf(fabsf(x), 128.f);
