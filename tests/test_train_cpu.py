@@ -257,3 +257,25 @@ def test_oracle_adamw_first_step():
 @pytest.mark.parametrize("T", [1 << 26, (1 << 31) - 1])
 def test_route_backward_of_more_tokens_than_a_launch_takes(T):
     assert ops.load_library().moe_route_backward(FAKE, FAKE, FAKE, T, 8, 1, FAKE, 0, None) == UNSUPPORTED
+
+
+def test_binding_refuses_a_tensor_twice():
+    p, q, g = (torch.zeros(8) for _ in range(3))
+    (m, v), (m2, v2) = ops.adamw_states(p), ops.adamw_states(p)
+    empty = torch.zeros(0)
+    call = lambda *lists, copies=None: ops.moe_adamw(*lists, lr=1e-3, step=1, copies=copies)  # noqa: E731
+    for args, copies in ((([p, p], [g, g], [m, m2], [v, v2]), None), (([p, q], [g, g], [m, m], [v, v2]), None),
+                         (([p], [g], [m], [m]), None), (([p], [g], [m], [v]), [p]),
+                         (([p, empty, empty, q], [g, empty, empty, g], [m, empty, empty, m], [v, empty, empty, v2]),
+                          None)):
+        with pytest.raises(ValueError, match="twice"):
+            call(*args, copies=copies)
+
+
+def test_binding_refuses_a_gradient_of_logits_over_its_inputs():
+    ids, w, g = torch.zeros(4, 8, dtype=torch.int32), torch.zeros(4, 8), torch.zeros(4, 8)
+    for out in (w, g):
+        with pytest.raises(ValueError, match="overlaps"):
+            ops.moe_route_backward(ids, w, g, 8, out=out)
+    with pytest.raises(ValueError):
+        ops.moe_grouped_gemm_backward_weights(w.bfloat16(), w.bfloat16(), torch.zeros(0, dtype=torch.int32))

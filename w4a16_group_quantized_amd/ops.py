@@ -1087,10 +1087,7 @@ def moe_grouped_gemm_backward_weights(grad: torch.Tensor, a: torch.Tensor,
     pa, a_code, sa, rows_a, K = _operand("a", a)
     if rows_a != rows or a_code != code:
         raise ValueError(f"a is {a.dtype} of {rows_a} rows, grad {grad.dtype} of {rows}")
-    po, E = None, 1
-    if expert_offsets is not None:
-        E = expert_offsets.numel() - 1
-        po = _dense("expert_offsets", expert_offsets, torch.int32, E + 1)
+    po, E = (None, 1) if expert_offsets is None else _segments(expert_offsets)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs the tensor to add to: pass out")
@@ -1174,6 +1171,7 @@ def moe_route_backward(topk_ids: torch.Tensor, topk_weights: torch.Tensor, grad_
     else:
         code = _DTYPE.get(out.dtype, -1)
         ptr = _dense("out", out, out.dtype if code >= 0 else torch.float32, T, E)
+        _apart("out", out, topk_ids=topk_ids, topk_weights=topk_weights, grad_weights=grad_weights)
     _run("moe_route_backward", _device_of(topk_ids, topk_weights, grad_weights, out), pi, pw, pg, T, E, k,
          ptr, code)
     return out
@@ -1206,9 +1204,10 @@ def adamw_state_values(state: tuple, signed: bool) -> torch.Tensor:
 def moe_adamw(params: list, grads: list, m: list, v: list, *, lr: float, beta1: float = 0.9,
               beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01, step: int,
               seed: int = 0, copies: list | None = None, grad_scale: torch.Tensor | None = None) -> None:
-    """One AdamW step, in place, over lists of tensors (adamw_states makes m and v; all of a call have
-    32 bits or all 8).  copies: 16-bit (or other) tensors, or None, that get the new parameters too.
-    seed (8 bits): another one at every step.  grad_scale: fp32 [1] on the device."""
+    """One AdamW step, in place, over lists of tensors, none of them twice (adamw_states makes m and v;
+    all of a call have 32 bits or all 8).  copies: 16-bit (or other) tensors, or None, that get the
+    new parameters too.  seed (8 bits): another one at every step.  grad_scale: fp32 [1] on the
+    device."""
     count = len(params)
     if len(grads) != count or len(m) != count or len(v) != count or (copies is not None
                                                                      and len(copies) != count):
@@ -1218,8 +1217,6 @@ def moe_adamw(params: list, grads: list, m: list, v: list, *, lr: float, beta1: 
         return
     bits = 8 if isinstance(m[0], tuple) else 32
     dev = params[0].get_device()
-    if dev < 0 or grad_scale is not None:
-        _device_of(params[0], grad_scale)
 
     # a column of the table: one loop over a list's tensors, which asks each as little as it can
     def column(name, tensors, sizes, dtype):
@@ -1268,6 +1265,13 @@ def moe_adamw(params: list, grads: list, m: list, v: list, *, lr: float, beta1: 
             for i in at:
                 (pc[i],), (code, *_) = typed("copies", [copies[i]], [ns[i]])
                 c_codes[i] = code
+    written = [*pp, *pm, *pv, *(c for c in pc if c)]
+    if len(set(written)) != len(written):
+        held = [x for x, n in zip([*pp, *pm, *pv, *pc], ns * 4) if n and x]
+        if len(set(held)) != len(held):
+            raise ValueError("a tensor is in params, m, v or copies twice")
+    if dev < 0 or grad_scale is not None:
+        _device_of(params[0], grad_scale)
     scale = None if grad_scale is None else _dense("grad_scale", grad_scale, torch.float32, 1)
     kinds = p_codes if g_codes == none else [a | b << 32 for a, b in zip(p_codes, g_codes)]
     table = [x for row in zip(ns, pp, pg, pm, pv, ms, vs, pc, kinds, c_codes) for x in row]
