@@ -281,3 +281,48 @@ def test_adamw_of_subnormal_second_moments(ops, bits, eps):
     m32, v32 = np.float32(1 - 0.9) * x, np.float32(1 - 0.999) * (x * x)  # in fp32, as the kernel's
     step = 1e-2 * (m32.astype(np.float64) / 0.1) / (np.sqrt(v32.astype(np.float64) / 0.001) + eps)
     assert (abs(np64(p) - (1 - step)) <= 2e-5 * abs(step) + 2.0 ** -23).all()
+
+
+# ---- sizes off the 16-byte grid ---------------------------------------------------------
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("counts,N,K", [([9000], 63, 65), ([3000, 0, 5000], 33, 130), ([20000], 3, 7), ([6000], 1, 1),
+                                        ([300, 2000], 257, 131)])
+def test_weight_gradient_of_odd_sizes_and_long_sums(ops, counts, N, K, out_dtype):
+    """Sums in parts and in one, plain and added to what is there, in a tensor with a value behind it."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    R, E = sum(counts), len(counts)
+    grad, a = (torch.randn((R, n), generator=g, device="cuda").to(BF16) for n in (N, K))
+    off = torch.tensor([0, *np.cumsum(counts)], dtype=torch.int32, device="cuda")
+    seg, g_h, a_h = off.cpu().numpy(), np64(grad), np64(a)
+    want, size = ref.product_weights(g_h, a_h, seg), ref.product_weights(abs(g_h), abs(a_h), seg)
+    half = torch.finfo(out_dtype).eps / 2
+    for accumulate in (False, True):
+        buf = torch.randn(E * N * K + 1, generator=g, device="cuda").to(out_dtype)
+        before = np64(buf)
+        held = before[:-1].reshape(E, N, K) * accumulate
+        got = np64(ops.moe_grouped_gemm_backward_weights(grad, a, off, out=buf[:-1].view(E, N, K), accumulate=accumulate))
+        tol = (max(counts) + 2) * 2.0 ** -23 * (size + abs(held)) + 1.01 * half * abs(want + held)
+        assert (abs(got - (want + held)) <= tol).all()
+        assert float(buf[-1]) == before[-1]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("E,R,N,K", [(3, 700, 521, 1031), (2, 2100, 1030, 513), (40, 3000, 259, 135)])
+def test_products_of_odd_sizes_in_large_tiles(ops, E, R, N, K, dtype):
+    """Rows behind and before the segments hold NaN, and the rows' ends another matrix's values."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    counts = np.bincount(np.random.default_rng(E).integers(0, E, R - 5), minlength=E)
+    off = torch.tensor(3 + np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    grad, a = (torch.randn((R, n + 3), generator=g, device="cuda").to(dtype)[:, 1:n + 1] for n in (N, K))
+    w = (torch.randn((E, N, K), generator=g, device="cuda") / K ** 0.5).to(dtype)
+    for t in (grad, a):
+        t[:3], t[-2:] = float("nan"), float("nan")
+    seg, g_h, a_h, w_h = off.cpu().numpy(), np64(grad), np64(a), np64(w)
+    mine = slice(3, R - 2)
+    for got, f, x, y, terms in ((ops.moe_grouped_gemm(a, w, off, dtype=F32), ref.product, a_h, w_h, K),
+                                (ops.moe_grouped_gemm_backward(grad, w, off, dtype=F32), ref.product_rows, g_h, w_h, N)):
+        size = f(abs(x), abs(y), seg)[mine]
+        assert (abs(np64(got)[mine] - f(x, y, seg)[mine]) <= (terms + 1) * 2.0 ** -23 * size).all()
+    got = np64(ops.moe_grouped_gemm_backward_weights(grad, a, off, dtype=F32))
+    size = ref.product_weights(abs(g_h), abs(a_h), seg)
+    assert (abs(got - ref.product_weights(g_h, a_h, seg)) <= (max(counts) + 1) * 2.0 ** -23 * size).all()

@@ -75,6 +75,15 @@ __device__ __forceinline__ void segment(const GroupedArgs& p, int e, int& r0, in
 
 constexpr int kGroupTiles = 4;
 constexpr int kChunk = 64;      // of the reduction
+
+// Part `n` of a segment: whole chunks to each part but the last.
+__device__ __forceinline__ void part_of(const GroupedArgs& p, int n, int& r0, int& r1) {
+  const int len = (p.by_parts(max(r1 - r0, 0) + p.parts - 1) + kChunk - 1) / kChunk * kChunk;
+  const int64_t from = r0 + static_cast<int64_t>(n) * len;
+  r0 = static_cast<int>(min(from, static_cast<int64_t>(r1)));
+  r1 = min(r1, static_cast<int>(min(from + len, static_cast<int64_t>(INT32_MAX))));
+}
+
 constexpr int kChunkRow = 128;  // bytes of it in a row
 
 // KS > 1 groups of WM x WN waves take KS chunks at once, one each, and add their sums in
@@ -236,12 +245,7 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
       const int e = p.by_parts(t.e);
       int r1;
       segment(p, e, t.r0, r1);
-      if (p.parts > 1) {  // whole chunks to each part but the last
-        const int len = (p.by_parts(max(r1 - t.r0, 0) + p.parts - 1) + kChunk - 1) / kChunk * kChunk;
-        const int64_t from = t.r0 + static_cast<int64_t>(t.e - e * p.parts) * len;
-        t.r0 = static_cast<int>(min(from, static_cast<int64_t>(r1)));
-        r1 = min(r1, static_cast<int>(min(from + len, static_cast<int64_t>(INT32_MAX))));
-      }
+      if (p.parts > 1) part_of(p, t.e - e * p.parts, t.r0, r1);
       t.depth = max(r1 - t.r0, 0);
     } else {
       place(tile, total, row, column);

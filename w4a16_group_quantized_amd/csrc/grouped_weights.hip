@@ -39,23 +39,33 @@ int parts_of(int64_t rows, int E, int N, int K) {
   return static_cast<int>(best);
 }
 
-// out = (what it holds +) the parts' sums, parts ascending; 4 elements per thread.
+// out = (what it holds +) the parts' sums, parts ascending; 4 elements per thread, of the
+// expert blockIdx.y.  Nothing here needs more than an element's alignment.
 template <typename TO>
 __global__ __launch_bounds__(256) void add_parts_kernel(const float* __restrict__ sums, int parts,
-                                                        int64_t n, int64_t total, int accumulate,
+                                                        int64_t n, int accumulate,
                                                         typename TO::bits* __restrict__ out) {
   const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (at >= total) return;
-  const int64_t e = at / n;  // n is a multiple of 4: N and K are of 8
-  const float* from = sums + e * parts * n + (at - e * n);
+  if (at >= n) return;
+  const int left = static_cast<int>(min(n - at, int64_t{4}));
+  const float* from = sums + blockIdx.y * parts * n + at;
+  out += blockIdx.y * n + at;
   f32x4 v{};
   if (accumulate) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = to_float(TO{}, out[at + i]);
+    for (int i = 0; i < 4; ++i)
+      if (i < left) v[i] = to_float(TO{}, out[i]);
   }
+  if (left == 4) {
 #pragma unroll 8
-  for (int p = 0; p < parts; ++p) v += *reinterpret_cast<const f32x4*>(from + p * n);
-  store4<TO>(out + at, 4, v);
+    for (int p = 0; p < parts; ++p) v += __builtin_bit_cast(f32x4, load16(from + p * n));
+  } else {
+    for (int p = 0; p < parts; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) v[i] += from[p * n + i];
+  }
+  store4<TO>(out, left, v);
 }
 
 }  // namespace
@@ -65,14 +75,31 @@ size_t grouped_workspace_bytes(int64_t rows, int E, int N, int K) {
   return parts > 1 ? static_cast<size_t>(E) * parts * N * K * sizeof(float) : 0;
 }
 
-void launch_grouped_weights(const GroupedArgs& a, hipStream_t stream) {
+GroupedArgs grouped_part_sums(const GroupedArgs& a) {
   GroupedArgs b = a;
   b.parts = parts_of(a.rows, a.E, a.N, a.K);
+  b.by_parts = Divisor(b.parts);
   if (b.parts > 1) {
     b.out = a.partial;
     b.out_dtype = MOE_F32;
     b.accumulate = 0;
   }
+  return b;
+}
+
+void launch_add_parts(const GroupedArgs& a, int parts, hipStream_t stream) {
+  if (parts == 1) return;
+  const int64_t n = static_cast<int64_t>(a.N) * a.K;
+  const dim3 grid(static_cast<unsigned>((n + 1023) / 1024), a.E);
+  with_dtype(a.out_dtype, [&](auto to) {
+    using TO = decltype(to);
+    hipLaunchKernelGGL((add_parts_kernel<TO>), grid, dim3(256), 0, stream, a.partial, parts, n,
+                       a.accumulate, static_cast<typename TO::bits*>(a.out));
+  });
+}
+
+void launch_grouped_weights(const GroupedArgs& a, hipStream_t stream) {
+  const GroupedArgs b = grouped_part_sums(a);
   const int size = size_of(static_cast<int64_t>(a.E) * b.parts, a.N, a.K);
   if (size == 256)
     launch_grouped_tiles<Grouped256, Product::kWeights>(b, stream);
@@ -80,14 +107,7 @@ void launch_grouped_weights(const GroupedArgs& a, hipStream_t stream) {
     launch_grouped_tiles<Grouped128, Product::kWeights>(b, stream);
   else
     launch_grouped_tiles<Grouped64, Product::kWeights>(b, stream);
-  if (b.parts == 1) return;
-  const int64_t n = static_cast<int64_t>(a.N) * a.K, total = n * a.E;
-  with_dtype(a.out_dtype, [&](auto to) {
-    using TO = decltype(to);
-    hipLaunchKernelGGL((add_parts_kernel<TO>), dim3(static_cast<unsigned>((total / 4 + 255) / 256)),
-                       dim3(256), 0, stream, a.partial, b.parts, n, total, a.accumulate,
-                       static_cast<typename TO::bits*>(a.out));
-  });
+  launch_add_parts(a, b.parts, stream);
 }
 
 }  // namespace moe

@@ -50,6 +50,10 @@ struct GroupedArgs {
   Divisor by_expert, by_group, by_parts;
 };
 size_t grouped_workspace_bytes(int64_t rows, int E, int N, int K);
+// kWeights in parts (grouped_weights.hip): the arguments of the parts' own sums in the
+// workspace, and the launch that adds them.
+GroupedArgs grouped_part_sums(const GroupedArgs& a);
+void launch_add_parts(const GroupedArgs& a, int parts, hipStream_t stream);
 // With tiles of 16-byte loads (grouped_out.hip, grouped_rows.hip, grouped_weights.hip).
 void launch_grouped_out(const GroupedArgs& a, hipStream_t stream);
 void launch_grouped_rows(const GroupedArgs& a, hipStream_t stream);

@@ -67,7 +67,8 @@ __device__ __forceinline__ void load8(const typename T::bits* p, int n, float (&
   }
 }
 
-template <typename T>
+// Nontemporal or not, as store16 says.
+template <typename T, bool ONCE = true>
 __device__ __forceinline__ void store8(typename T::bits* p, int n, const float (&v)[8]) {
   if (n >= 8) {
     constexpr int E = 16 / kBytes<T>;
@@ -82,7 +83,10 @@ __device__ __forceinline__ void store8(typename T::bits* p, int n, const float (
           d[j] = static_cast<uint32_t>(from_float(T{}, v[i + 2 * j])) |
                  (static_cast<uint32_t>(from_float(T{}, v[i + 2 * j + 1])) << 16);
       }
-      store16(p + i, d);
+      if constexpr (ONCE)
+        store16(p + i, d);
+      else
+        reinterpret_cast<Unaligned16*>(p + i)->d = d;
     }
   } else {
 #pragma unroll
