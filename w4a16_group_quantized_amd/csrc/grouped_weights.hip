@@ -33,9 +33,11 @@ int parts_of(int64_t rows, int E, int N, int K) {
     const int64_t sums = chunks * cost_of(size, tiles_of(blocks, N, K, size));
     return parts == 1 ? sums : sums + kLaunch + blocks * N * K * 4 / kBytesPerUnit;
   };
-  int64_t best = 1;
-  for (int64_t parts = 2; parts <= 32 && parts * E * 256 <= rows; ++parts)
-    if (cost(parts) < cost(best)) best = parts;
+  int64_t best = 1, least = cost(1);
+  for (int64_t parts = 2; parts <= 32 && parts * E * 256 <= rows; ++parts) {
+    const int64_t c = cost(parts);
+    if (c < least) best = parts, least = c;
+  }
   return static_cast<int>(best);
 }
 
