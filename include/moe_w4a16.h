@@ -847,7 +847,9 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_weights,
  *       - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
  * in fp32; p is rounded once to its type (and once to copy's), and is updated
  * from m and v before these are rounded to their states.  With eps 0 an element
- * whose v is 0 divides by 0.
+ * whose v is 0 divides by 0; a positive eps may be as small as it likes (fp32
+ * holds it as 2^-149 at least), and an element whose m and v are 0 then moves by
+ * its weight decay alone.
  *
  * States of 8 bits: elements in blocks of MOE_ADAMW_BLOCK (the last may be
  * short), per block one fp32 scale = largest magnitude / 1.875.  A code's

@@ -1,0 +1,49 @@
+"""GPU: AdamW at the ends of its scalars' ranges, against the formula in 64 bits."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def ops():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from w4a16_group_quantized_amd import ops
+
+    ops.load_library()
+    return ops
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# ---- eps below fp32's normal numbers ------------------------------------------------------
+@pytest.mark.parametrize("eps", [1e-37, 1e-38, 1e-40, 1e-45, 1e-50])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_of_a_subnormal_eps(ops, bits, eps):
+    """Elements without moments (an expert that had no tokens) stay as they are; those whose second moment
+    underflows are divided by eps, which fp32 holds as its smallest number at least; the others do not see it."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    n = 3000
+    grad = torch.randn(n, generator=g, device="cuda")
+    grad[::3] = 0.0
+    grad[1::3] = 1e-24
+    p = torch.randn(n, generator=g, device="cuda")
+    before, x = np64(p), np64(grad)
+    m, v = ops.adamw_states(p, bits)
+    ops.moe_adamw([p], [grad], [m], [v], lr=1e-2, beta1=0.9, beta2=0.999, eps=eps, weight_decay=0.0, step=1, seed=1)
+    got, held = np64(p), max(float(np.float32(eps)), 2.0 ** -149)
+    assert np.array_equal(got[::3], before[::3])
+    root = np.where(abs(x) > 1e-20, abs(x), 0.0)  # sqrt(v / (1 - beta2)); 0.001 * 1e-48 is 0 in fp32
+    for part in (slice(1, None, 3), slice(2, None, 3)):
+        step = 1e-2 * x[part] / (root[part] + held)
+        # twelve roundings of 2^-24 at most (scalars, moments, root, reciprocal, products), and p's own
+        want = before[part] - step
+        assert (abs(got[part] - want) <= 12 * 2.0 ** -24 * abs(step) + 2.0 ** -24 * abs(want)).all()

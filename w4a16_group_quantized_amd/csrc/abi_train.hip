@@ -239,7 +239,8 @@ int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, int32_t state_bits
   s.keep = static_cast<float>(1 - lr * weight_decay);
   s.size = static_cast<float>(lr / (1 - pow(beta1, static_cast<double>(step))));
   s.root = static_cast<float>(1 / sqrt(1 - pow(beta2, static_cast<double>(step))));
-  s.eps = static_cast<float>(eps);
+  // a positive eps stays positive: an element without moments moves by 0 / eps = 0
+  s.eps = eps > 0 ? fmaxf(static_cast<float>(eps), 0x1p-149f) : 0.f;
   s.grad_scale = grad_scale;
   s.seed = seed;
   s.small = ldexp(static_cast<double>(s.root), -63) > ldexp(static_cast<double>(s.eps), -25);

@@ -186,22 +186,25 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Batch b, AdamwScalars s
       v[i] = s.beta2 * v[i] + s.rest2 * (gi * gi);
     }
   }
-  float root[8];
-  if (s.small) {  // the root's instruction takes v under 2^-126 for 0
+  float move[8];  // m / (sqrt(v) / sqrt(c2) + eps)
+  if (s.small) {
+    // The root's instruction takes v under 2^-126 for 0, and the reciprocal's an eps under it;
+    // where eps is all there is, its reciprocal may also be past fp32's range while m is 0.
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const bool tiny = v[i] < 0x1p-96f;
-      root[i] = __builtin_amdgcn_sqrtf(v[i] * (tiny ? 0x1p64f : 1.f)) * (tiny ? 0x1p-32f : 1.f);
+      const float root =
+          __builtin_amdgcn_sqrtf(v[i] * (tiny ? 0x1p64f : 1.f)) * (tiny ? 0x1p-32f : 1.f);
+      const float over = fmaf(root, s.root, s.eps), up = over < 0x1p-64f ? 0x1p64f : 1.f;
+      move[i] = m[i] * up * __builtin_amdgcn_rcpf(over * up);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) root[i] = __builtin_amdgcn_sqrtf(v[i]);
+    for (int i = 0; i < 8; ++i)
+      move[i] = m[i] * __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_sqrtf(v[i]), s.root, s.eps));
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float over = fmaf(root[i], s.root, s.eps);
-    p[i] = fmaf(-s.size, m[i] * __builtin_amdgcn_rcpf(over), p[i] * s.keep);
-  }
+  for (int i = 0; i < 8; ++i) p[i] = fmaf(-s.size, move[i], p[i] * s.keep);
   if constexpr (BITS == 8) {
     uint32_t noise[8], more[8];
 #pragma unroll

@@ -83,7 +83,7 @@ struct AdamwScalars {
   float keep, size, root, eps;       // 1 - lr wd, lr / c1, 1 / sqrt(c2)
   const float* grad_scale;           // device, or null: 1
   uint32_t seed;
-  int small;                         // eps does not cover the root of v = 2^-126
+  int small;                         // eps does not cover the root of v = 2^-126, or is under it
 };
 void launch_adamw(const moe_adamw_tensor* tensors, int count, int state_bits,
                   const AdamwScalars& s, hipStream_t stream);
