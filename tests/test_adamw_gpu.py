@@ -47,3 +47,30 @@ def test_adamw_of_a_subnormal_eps(ops, bits, eps):
         # twelve roundings of 2^-24 at most (scalars, moments, root, reciprocal, products), and p's own
         want = before[part] - step
         assert (abs(got[part] - want) <= 12 * 2.0 ** -24 * abs(step) + 2.0 ** -24 * abs(want)).all()
+
+
+# ---- weight decays next to fp32's steps ---------------------------------------------------
+@pytest.mark.parametrize("lr,decay", [(1e-3, 0.01), (1e-5, 0.01), (1e-6, 0.031), (1e-6, 0.01), (0.5, 1.0), (1.0, 1.0)])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_of_a_small_weight_decay(ops, bits, lr, decay):
+    """Without gradients a parameter becomes p (1 - lr wd), rounded once: decays of a few fp32 steps or less
+    are not rounded to whole steps first."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    p = 4 * torch.randn(1 << 14, generator=g, device="cuda")
+    before = np64(p)
+    m, v = ops.adamw_states(p, bits)
+    ops.moe_adamw([p], [torch.zeros_like(p)], [m], [v], lr=lr, weight_decay=decay, step=3, seed=1)
+    move = lr * decay * before
+    want = before - move
+    # half of fp32's step there; the move's factor and product are rounded to 2^-24 each
+    tol = np.spacing(abs(want).astype(np.float32)).astype(np.float64) / 2 + 3 * 2.0 ** -24 * abs(move)
+    assert (abs(np64(p) - want) <= tol).all()
+
+
+def test_adamw_of_infinite_parameters(ops):
+    """An infinity stays one, with decay or without."""
+    for decay in (0.0, 0.1):
+        p = torch.tensor([float("inf"), -float("inf"), 1.0], device="cuda")
+        m, v = ops.adamw_states(p)
+        ops.moe_adamw([p], [torch.ones(3, device="cuda")], [m], [v], lr=1e-3, weight_decay=decay, step=1)
+        assert p[0] == float("inf") and p[1] == -float("inf") and p[2].isfinite()

@@ -236,7 +236,7 @@ int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, int32_t state_bits
   s.rest1 = static_cast<float>(1 - beta1);
   s.beta2 = static_cast<float>(beta2);
   s.rest2 = static_cast<float>(1 - beta2);
-  s.keep = static_cast<float>(1 - lr * weight_decay);
+  s.decay = static_cast<float>(lr * weight_decay);
   s.size = static_cast<float>(lr / (1 - pow(beta1, static_cast<double>(step))));
   s.root = static_cast<float>(1 / sqrt(1 - pow(beta2, static_cast<double>(step))));
   // a positive eps stays positive: an element without moments moves by 0 / eps = 0

@@ -22,6 +22,8 @@
 #include "train.h"
 #include "typed.h"
 
+#include <float.h>
+
 namespace moe {
 namespace {
 
@@ -203,8 +205,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Batch b, AdamwScalars s
     for (int i = 0; i < 8; ++i)
       move[i] = m[i] * __builtin_amdgcn_rcpf(fmaf(__builtin_amdgcn_sqrtf(v[i]), s.root, s.eps));
   }
+  // Both parts of the change are summed and p is rounded once: as a factor, 1 - lr wd is held in
+  // steps of 2^-24, and a decay of a few of them would be off by as much of it (1e-7: 19 %).  An
+  // infinity stays one: its decay is a finite number.
 #pragma unroll
-  for (int i = 0; i < 8; ++i) p[i] = fmaf(-s.size, move[i], p[i] * s.keep);
+  for (int i = 0; i < 8; ++i)
+    p[i] -= fmaf(s.size, move[i], s.decay * __builtin_amdgcn_fmed3f(p[i], -FLT_MAX, FLT_MAX));
   if constexpr (BITS == 8) {
     uint32_t noise[8], more[8];
 #pragma unroll

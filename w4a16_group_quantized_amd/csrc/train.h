@@ -80,7 +80,7 @@ void launch_route_backward(const int* ids, const float* weights, const float* gr
 
 struct AdamwScalars {
   float beta1, rest1, beta2, rest2;  // rest = 1 - beta
-  float keep, size, root, eps;       // 1 - lr wd, lr / c1, 1 / sqrt(c2)
+  float decay, size, root, eps;      // lr wd, lr / c1, 1 / sqrt(c2)
   const float* grad_scale;           // device, or null: 1
   uint32_t seed;
   int small;                         // eps does not cover the root of v = 2^-126, or is under it
