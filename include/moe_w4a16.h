@@ -876,11 +876,13 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_weights,
  *   grad_scale  in   fp32 [1] on the device, or NULL: 1 (clipping and loss
  *                    scales without a synchronisation)
  *
- * No two buffers of a call may overlap.  The scalars are the call's: a captured
- * graph repeats its step number, rate and seed when it is replayed.
+ * A buffer that the call writes must not overlap another of the call; gradients
+ * may share theirs among them.  The scalars are the call's: a captured graph
+ * repeats its step number, rate and seed when it is replayed.
  *
  * MOE_ERR_INVALID_ARG for state_bits, betas outside [0, 1), negative or
- * non-finite lr, eps or weight_decay, step < 1.  Limits: n <= 2^33.
+ * non-finite lr, eps or weight_decay, step < 1, buffers that overlap.  Limits:
+ * n <= 2^33.
  */
 #define MOE_ADAMW_BLOCK 128
 typedef struct moe_adamw_tensor {

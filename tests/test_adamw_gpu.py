@@ -74,3 +74,43 @@ def test_adamw_of_infinite_parameters(ops):
         m, v = ops.adamw_states(p)
         ops.moe_adamw([p], [torch.ones(3, device="cuda")], [m], [v], lr=1e-3, weight_decay=decay, step=1)
         assert p[0] == float("inf") and p[1] == -float("inf") and p[2].isfinite()
+
+
+# ---- tensors side by side, and tensors that share memory ----------------------------------
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_of_views_side_by_side(ops, bits):
+    """Neighbours in one buffer and one gradient for several tensors are taken, as if each were alone;
+    a scales buffer that two tensors share, or a shifted view, is refused and nothing changes."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    sizes, count = [128, 256, 384], 3
+    ends = np.cumsum(sizes)
+    flat = torch.randn(int(ends[-1]), generator=g, device="cuda")
+    whole_m, whole_v = ops.adamw_states(flat, bits)
+    grad = torch.randn(384, generator=g, device="cuda")
+
+    def part(state, i):
+        cut = lambda t, unit: t[(ends[i] - sizes[i]) // unit: ends[i] // unit]  # noqa: E731
+        return cut(state, 1) if bits == 32 else (cut(state[0], 1), cut(state[1], ops.ADAMW_BLOCK))
+
+    ps = [flat[e - n: e] for e, n in zip(ends, sizes)]
+    ms, vs = [part(whole_m, i) for i in range(count)], [part(whole_v, i) for i in range(count)]
+    gs = [grad[:n] for n in sizes]
+    alone = [p.clone() for p in ps]
+    kw = dict(lr=1e-2, step=1, seed=3)
+    for p, x in zip(alone, gs):
+        m, v = ops.adamw_states(p, bits)
+        ops.moe_adamw([p], [x], [m], [v], **kw)
+    ops.moe_adamw(ps, gs, ms, vs, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(ps, alone))
+    before = flat.clone()
+    states = lambda: map(list, zip(*(ops.adamw_states(grad, bits) for _ in range(2))))  # noqa: E731
+    with pytest.raises(ValueError, match="overlaps"):
+        ops.moe_adamw([flat[:384], flat[383:767]], [grad, grad], *states(), **kw)
+    with pytest.raises(ValueError, match="overlaps"):
+        ops.moe_adamw([flat[:384]], [grad], [ms[2]], [vs[2]], grad_scale=flat[7:8], **kw)
+    if bits == 8:
+        m, v = states()
+        m[1] = (m[1][0], m[0][1])
+        with pytest.raises(ValueError, match="m scales"):
+            ops.moe_adamw([flat[:384], flat[384:]], [grad, grad], m, v, **kw)
+    assert torch.equal(flat, before)

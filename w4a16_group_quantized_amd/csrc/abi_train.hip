@@ -1,10 +1,13 @@
 // C ABI of the training operators: argument validation and dispatch.
 // Declarations and the full contract are in include/moe_w4a16.h.  Nothing here
-// allocates, frees or synchronises.
+// allocates or frees device memory, or synchronises.
 #include "train.h"
 #include "typed.h"
 
 #include <math.h>
+#include <stdlib.h>
+
+#include <algorithm>
 
 namespace {
 
@@ -75,6 +78,63 @@ int check_act(int32_t dtype, int64_t rows, int32_t I, const int32_t* offsets, in
     return MOE_ERR_UNSUPPORTED;
   // one thread per 8 columns, numbered with 32 bits
   return rows * ((I + 7) / 8) >= (static_cast<int64_t>(1) << 32) - 256 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// f(address, bytes) for each buffer that an AdamW step of a tensor writes.
+template <typename F>
+void adamw_written(const moe_adamw_tensor& t, int32_t state_bits, F&& f) {
+  const uint64_t n = static_cast<uint64_t>(t.n), blocks = (n + kAdamwBlock - 1) / kAdamwBlock;
+  const auto put = [&](const void* p, uint64_t bytes) { f(reinterpret_cast<uint64_t>(p), bytes); };
+  put(t.param, n * dtype_bytes(t.param_dtype));
+  put(t.m, n * (state_bits / 8));
+  put(t.v, n * (state_bits / 8));
+  if (state_bits == 8) {
+    put(t.m_scales, blocks * sizeof(float));
+    put(t.v_scales, blocks * sizeof(float));
+  }
+  if (t.copy != nullptr) put(t.copy, n * dtype_bytes(t.copy_dtype));
+}
+
+// Whether a buffer that the step writes shares memory with any other of the call: ranges are
+// apart when their sorted beginnings and ends take turns.  Gradients and the scale of theirs
+// are only read, and may share theirs among them.  The ranges' place is the host's.
+int check_apart(const moe_adamw_tensor* tensors, int32_t count, int32_t state_bits,
+                const float* grad_scale) {
+  constexpr size_t kNear = 512;  // 4 KB on the stack each: 170 tensors with states in fp32
+  uint64_t near_begins[kNear], near_ends[kNear];
+  size_t n = 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (tensors[i].n > 0) adamw_written(tensors[i], state_bits, [&](uint64_t, uint64_t) { ++n; });
+  uint64_t* far = nullptr;
+  if (n > kNear) {
+    far = static_cast<uint64_t*>(malloc(2 * n * sizeof(uint64_t)));
+    if (far == nullptr) return MOE_ERR_UNSUPPORTED;
+  }
+  uint64_t* begins = far != nullptr ? far : near_begins;
+  uint64_t* ends = far != nullptr ? far + n : near_ends;
+  size_t at = 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (tensors[i].n > 0)
+      adamw_written(tensors[i], state_bits, [&](uint64_t p, uint64_t bytes) {
+        begins[at] = p;
+        ends[at++] = p + bytes;
+      });
+  std::sort(begins, begins + n);
+  std::sort(ends, ends + n);
+  bool apart = true;
+  for (size_t i = 1; i < n; ++i) apart = apart && ends[i - 1] <= begins[i];
+  // a range that is only read: the first written one that ends behind its beginning
+  const auto clear = [&](const void* p, uint64_t bytes) {
+    const uint64_t from = reinterpret_cast<uint64_t>(p);
+    const size_t next = std::upper_bound(ends, ends + n, from) - ends;
+    return next == n || from + bytes <= begins[next];
+  };
+  for (int32_t i = 0; apart && i < count; ++i)
+    if (tensors[i].n > 0)
+      apart = clear(tensors[i].grad, static_cast<uint64_t>(tensors[i].n) * dtype_bytes(tensors[i].grad_dtype));
+  if (apart && grad_scale != nullptr) apart = clear(grad_scale, sizeof(float));
+  free(far);
+  return apart ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 
 }  // namespace
@@ -231,6 +291,7 @@ int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, int32_t state_bits
     }
   }
   if (!any) return MOE_OK;
+  if (int st = check_apart(tensors, count, state_bits, grad_scale)) return st;
   AdamwScalars s;
   s.beta1 = static_cast<float>(beta1);
   s.rest1 = static_cast<float>(1 - beta1);

@@ -1205,13 +1205,28 @@ def adamw_state_values(state: tuple, signed: bool) -> torch.Tensor:
     return (torch.where(c > 127, -value, value) if signed else value).view(codes.shape)
 
 
+def _apart_lists(written: dict, read: dict) -> None:
+    """Refuses lists of contiguous tensors of which one that is written shares memory with another."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes, f"{name}[{i}]", lists is written)
+                   for lists in (written, read) for name, tensors in lists.items()
+                   for i, t in enumerate(tensors) if t is not None and t.numel())
+    ends = [(0, ""), (0, "")]  # of the spans before: the furthest end of all, and of the written ones
+    for begin, end, name, writes in spans:
+        reach, other = ends[0 if writes else 1]
+        if reach > begin:
+            raise ValueError(f"{name} overlaps {other}: a tensor that is written is in the call twice")
+        ends[0] = max(ends[0], (end, name))
+        if writes:
+            ends[1] = max(ends[1], (end, name))
+
+
 def moe_adamw(params: list, grads: list, m: list, v: list, *, lr: float, beta1: float = 0.9,
               beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01, step: int,
               seed: int = 0, copies: list | None = None, grad_scale: torch.Tensor | None = None) -> None:
-    """One AdamW step, in place, over lists of tensors, none of them twice (adamw_states makes m and v;
-    all of a call have 32 bits or all 8).  copies: 16-bit (or other) tensors, or None, that get the
-    new parameters too.  seed (8 bits): another one at every step.  grad_scale: fp32 [1] on the
-    device."""
+    """One AdamW step, in place, over lists of tensors (adamw_states makes m and v; all of a call have
+    32 bits or all 8).  None that is written may share memory with another.  copies: 16-bit (or
+    other) tensors, or None, that get the new parameters too.  seed (8 bits): another one at every
+    step.  grad_scale: fp32 [1] on the device."""
     count = len(params)
     if len(grads) != count or len(m) != count or len(v) != count or (copies is not None
                                                                      and len(copies) != count):
@@ -1256,9 +1271,10 @@ def moe_adamw(params: list, grads: list, m: list, v: list, *, lr: float, beta1: 
         ms = vs = none
     else:
         blocks = [(n + ADAMW_BLOCK - 1) // ADAMW_BLOCK for n in ns]
-        (mc, ms), (vc, vs) = zip(*m), zip(*v)
+        (mc, m_scales), (vc, v_scales) = zip(*m), zip(*v)
         pm, pv = column("m codes", mc, ns, torch.uint8), column("v codes", vc, ns, torch.uint8)
-        ms, vs = column("m scales", ms, blocks, torch.float32), column("v scales", vs, blocks, torch.float32)
+        ms = column("m scales", m_scales, blocks, torch.float32)
+        vs = column("v scales", v_scales, blocks, torch.float32)
     pc, c_codes = none, none
     if copies is not None:
         at = [i for i, c in enumerate(copies) if c is not None]
@@ -1269,15 +1285,26 @@ def moe_adamw(params: list, grads: list, m: list, v: list, *, lr: float, beta1: 
             for i in at:
                 (pc[i],), (code, *_) = typed("copies", [copies[i]], [ns[i]])
                 c_codes[i] = code
-    written = [*pp, *pm, *pv, *(c for c in pc if c)]
-    if len(set(written)) != len(written):
-        held = [x for x, n in zip([*pp, *pm, *pv, *pc], ns * 4) if n and x]
-        if len(set(held)) != len(held):
-            raise ValueError("a tensor is in params, m, v or copies twice")
-    if dev < 0 or grad_scale is not None:
-        _device_of(params[0], grad_scale)
+
+    def apart():  # the library refuses tensors that share memory: this says which
+        written, read = {"params": params, "m": m, "v": v, "copies": copies or ()}, {"grads": grads}
+        if bits == 8:
+            written |= {"m": mc, "m scales": m_scales, "v": vc, "v scales": v_scales}
+        if grad_scale is not None:
+            read["grad_scale"] = [grad_scale]
+        _apart_lists(written, read)
+
     scale = None if grad_scale is None else _dense("grad_scale", grad_scale, torch.float32, 1)
+    if dev < 0 or grad_scale is not None:
+        if dev < 0:
+            apart()
+        _device_of(params[0], grad_scale)
     kinds = p_codes if g_codes == none else [a | b << 32 for a, b in zip(p_codes, g_codes)]
     table = itertools.chain.from_iterable(zip(ns, pp, pg, pm, pv, ms, vs, pc, kinds, c_codes))
-    _run("moe_adamw", dev, struct.pack(f"{10 * count}q", *table), count, bits, lr, beta1, beta2, eps, weight_decay,
-         step, seed & 0xFFFFFFFF, scale)
+    try:
+        _run("moe_adamw", dev, struct.pack(f"{10 * count}q", *table), count, bits, lr, beta1, beta2, eps,
+             weight_decay, step, seed & 0xFFFFFFFF, scale)
+    except MoEError as error:
+        if error.status == MOE_ERR_INVALID_ARG:
+            apart()
+        raise
