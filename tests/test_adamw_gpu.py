@@ -114,3 +114,19 @@ def test_adamw_of_views_side_by_side(ops, bits):
         with pytest.raises(ValueError, match="m scales"):
             ops.moe_adamw([flat[:384], flat[384:]], [grad, grad], m, v, **kw)
     assert torch.equal(flat, before)
+
+
+# ---- what the rounding of 8-bit states goes by --------------------------------------------
+def test_adamw_without_a_seed_rounds_by_the_step(ops):
+    """The same states and gradients at two steps are rounded differently; the step's number is the seed."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    grad = torch.randn(4096, generator=g, device="cuda")
+    out = []
+    for kw in (dict(step=1), dict(step=2), dict(step=2, seed=2), dict(step=(1 << 32) + 2)):
+        p = torch.zeros(4096, device="cuda")
+        m, v = ops.adamw_states(p, 8)
+        ops.moe_adamw([p], [grad], [m], [v], lr=1e-3, **kw)
+        out.append((m[0], v[0]))
+    same = lambda a, b: all(torch.equal(x, y) for x, y in zip(a, b))  # noqa: E731
+    assert not torch.equal(out[0][0], out[1][0]) and not torch.equal(out[0][1], out[1][1])
+    assert same(out[1], out[2]) and same(out[1], out[3])

@@ -1222,11 +1222,12 @@ def _apart_lists(written: dict, read: dict) -> None:
 
 def moe_adamw(params: list, grads: list, m: list, v: list, *, lr: float, beta1: float = 0.9,
               beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01, step: int,
-              seed: int = 0, copies: list | None = None, grad_scale: torch.Tensor | None = None) -> None:
+              seed: int | None = None, copies: list | None = None, grad_scale: torch.Tensor | None = None) -> None:
     """One AdamW step, in place, over lists of tensors (adamw_states makes m and v; all of a call have
     32 bits or all 8).  None that is written may share memory with another.  copies: 16-bit (or
-    other) tensors, or None, that get the new parameters too.  seed (8 bits): another one at every
-    step.  grad_scale: fp32 [1] on the device."""
+    other) tensors, or None, that get the new parameters too.  seed (8 bits; default: step): another
+    one at every step, or the same elements are rounded up every time, and another one in each of
+    the calls that share a step.  grad_scale: fp32 [1] on the device."""
     count = len(params)
     if len(grads) != count or len(m) != count or len(v) != count or (copies is not None
                                                                      and len(copies) != count):
@@ -1303,7 +1304,7 @@ def moe_adamw(params: list, grads: list, m: list, v: list, *, lr: float, beta1: 
     table = itertools.chain.from_iterable(zip(ns, pp, pg, pm, pv, ms, vs, pc, kinds, c_codes))
     try:
         _run("moe_adamw", dev, struct.pack(f"{10 * count}q", *table), count, bits, lr, beta1, beta2, eps,
-             weight_decay, step, seed & 0xFFFFFFFF, scale)
+             weight_decay, step, (step if seed is None else seed) & 0xFFFFFFFF, scale)
     except MoEError as error:
         if error.status == MOE_ERR_INVALID_ARG:
             apart()
