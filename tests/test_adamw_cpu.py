@@ -1,10 +1,12 @@
-"""CPU: what AdamW refuses before anything reaches a GPU."""
+"""CPU: what AdamW refuses before anything reaches a GPU, and how its 8-bit states have to be rounded."""
 
 import ctypes
 import os
 
+import numpy as np
 import pytest
 
+from oracle import train_oracle as ref
 from w4a16_group_quantized_amd import ops
 
 torch = pytest.importorskip("torch")
@@ -93,3 +95,41 @@ def test_binding_names_tensors_that_overlap():
             (([p, q], [g, g], [m, m2], [v, v2]), {}, "not on a GPU")):
         with pytest.raises(ValueError, match=match):
             call(*args, **kw)
+
+
+# ---- why states are rounded by chance, and by another one at every step -------------------
+def decays(signed, beta, steps, round_codes):
+    """What is left of an 8-bit state's sum, over what should be, when one element per block keeps its block's
+    scale and the others, between a quarter and the whole of a unit, get no gradients."""
+    n = 1 << 13
+    x = np.random.default_rng(0).uniform(0.25, 1.0, n)
+    x[:: ref.BLOCK] = 3.0
+    held = np.arange(n) % ref.BLOCK == 0
+    scale = np.repeat(ref.block_scales(x), ref.BLOCK)
+    values = ref.code_values(signed)
+    x = values[round_codes(x, scale, 0, signed)] * scale
+    first = x[~held].sum()
+    for step in range(1, steps + 1):
+        x = np.where(held, 3.0, beta * x)
+        x = values[round_codes(x, scale, step, signed)] * scale
+    return x[~held].sum() / first / beta ** steps
+
+
+@pytest.mark.parametrize("signed,beta,steps", [(False, 0.999, 300), (True, 0.99, 60)])
+def test_moments_follow_only_with_another_noise_each_step(signed, beta, steps):
+    def by(noise):
+        return lambda x, scale, step, signed: ref.code_sizes(x, scale, noise(x.size, step), signed)
+
+    which = 0 if signed else 1
+    each = decays(signed, beta, steps, by(lambda n, step: ref.noise(n, step, which) / 2.0 ** 20))
+    once = decays(signed, beta, steps, by(lambda n, step: ref.noise(n, 0, which) / 2.0 ** 20))
+    near = decays(signed, beta, steps, by(lambda n, step: np.full(n, 0.5)))
+    # A code's step is at most an eighth of its value x, and a decay of (1 - beta) x is rounded to it or not: a
+    # variance of (1 - beta) x^2 / 8 at most.  Over the steps and elements, x^2 in the mean 1.12 times the mean's
+    # square, the sum's deviation is sqrt(steps (1 - beta) / 8 * 1.12 / n) of the first sum: five of them, over
+    # what is left
+    five = 5 * (steps * (1 - beta) / 8 * 1.12 / (1 << 13)) ** 0.5 / beta ** steps
+    assert abs(each - 1) < five
+    # the nearest code is the same one again where (1 - beta) is under half of a sixteenth: nothing decays
+    assert near == pytest.approx(beta ** -steps)
+    assert abs(once - 1) > 2 * five

@@ -130,3 +130,35 @@ def test_adamw_without_a_seed_rounds_by_the_step(ops):
     same = lambda a, b: all(torch.equal(x, y) for x, y in zip(a, b))  # noqa: E731
     assert not torch.equal(out[0][0], out[1][0]) and not torch.equal(out[0][1], out[1][1])
     assert same(out[1], out[2]) and same(out[1], out[3])
+
+
+@pytest.mark.parametrize("kind", ["seeds", "no seed"])
+@pytest.mark.parametrize("which,beta,steps", [("v", 0.999, 300), ("m", 0.99, 60)])
+def test_adamw_8bit_moments_decay_under_a_held_scale(ops, which, beta, steps, kind):
+    """One element of each block has a gradient that keeps its moment, and with it the block's scale, where it is;
+    the others had one gradient and decay to beta^steps.  Codes rounded to nearest, or by the same noise at
+    every step, stand still."""
+    n, signed = 1 << 16, which == "m"
+    g = torch.Generator(device="cuda").manual_seed(3)
+    first = 0.25 + 0.75 * torch.rand(n, generator=g, device="cuda")  # the moment, over 1 - beta
+    held = torch.arange(n, device="cuda") % ops.ADAMW_BLOCK == 0
+    first[held] = 3.0
+    keep = torch.where(held, 3.0 * (1 - beta), 0.0)                  # beta M + (1 - beta) M = M = 3 (1 - beta)
+    if which == "v":
+        first, keep = first.sqrt(), keep.sqrt()
+    p = torch.zeros(n, device="cuda")
+    m, v = ops.adamw_states(p, 8)
+    state = m if signed else v
+    hyper = dict(lr=1e-3, weight_decay=0.0, beta1=beta if signed else 0.9, beta2=0.999 if signed else beta)
+    seed = (lambda step: {"seed": 1000 - step}) if kind == "seeds" else (lambda step: {})
+    ops.moe_adamw([p], [first], [m], [v], step=1, **seed(1), **hyper)
+    before = ops.adamw_state_values(state, signed).double()
+    for step in range(2, steps + 2):
+        ops.moe_adamw([p], [keep], [m], [v], step=step, **seed(step), **hyper)
+    after = ops.adamw_state_values(state, signed).double()
+    # fp32 roundings of the held moment, 2^-22 a step at most
+    assert torch.allclose(after[held], before[held], rtol=steps * 2.0 ** -22, atol=0)
+    # a rounding's variance is (1 - beta) x^2 / 8 at most (a code's step is an eighth of x or less), and the mean of
+    # x^2 1.12 times the mean's square: five deviations of the sum over steps and elements
+    five = 5 * (steps * (1 - beta) / 8 * 1.12 / n) ** 0.5 / beta ** steps
+    assert abs(float(after[~held].sum() / before[~held].sum()) / beta ** steps - 1) < five

@@ -15,7 +15,8 @@
 // one formula takes all).  Back to a code: add 20 noise bits behind the 3 mantissa
 // bits and cut.  That rounds up with the probability of the part cut off, so the
 // mean of many steps follows the moments; to nearest, a step's change of
-// (1 - b2) = 0.1% would never pass half of a code's 6% and v would stand still.
+// (1 - b2) = 0.1% would never pass half of a code's 6% and v would stand still under
+// a scale that does (300 steps: 35% too large; with one noise for all steps 34%).
 // The noise is a mix of the element's number and the step's seed, so a step is a
 // function of its arguments.  A positive v never becomes 0: next to an m that did
 // not, it would divide by eps.
