@@ -832,7 +832,7 @@ int moe_silu_mul_backward(const void* grad_act, int64_t grad_stride,
  *   grad_weights  in   fp32 [T, top_k]
  *   grad_logits   out  out_dtype [T, E]; must not overlap an input
  *
- * Limits: 1 <= E <= 4096; 1 <= top_k <= 64; T < 2^26; T * top_k < 2^31.
+ * Limits: 1 <= E <= 4096; 1 <= top_k <= 64; T <= 2^26 - 4; T * top_k < 2^31.
  */
 int moe_route_backward(const int32_t* topk_ids, const float* topk_weights,
                        const float* grad_weights, int64_t T, int32_t E,

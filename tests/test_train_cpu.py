@@ -279,3 +279,9 @@ def test_binding_refuses_a_gradient_of_logits_over_its_inputs():
             ops.moe_route_backward(ids, w, g, 8, out=out)
     with pytest.raises(ValueError):
         ops.moe_grouped_gemm_backward_weights(w.bfloat16(), w.bfloat16(), torch.zeros(0, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("T", [(1 << 26) - 3, (1 << 26) - 1])
+def test_route_backward_of_the_last_tokens_that_make_a_launch_too_long(T):
+    """Four tokens to a workgroup of 256 threads: one token behind 2^26 - 4 is the 2^24th workgroup."""
+    assert ops.load_library().moe_route_backward(FAKE, FAKE, FAKE, T, 8, 1, FAKE, 0, None) == UNSUPPORTED

@@ -326,3 +326,17 @@ def test_products_of_odd_sizes_in_large_tiles(ops, E, R, N, K, dtype):
     got = np64(ops.moe_grouped_gemm_backward_weights(grad, a, off, dtype=F32))
     size = ref.product_weights(abs(g_h), abs(a_h), seg)
     assert (abs(got - ref.product_weights(g_h, a_h, seg)) <= (max(counts) + 1) * 2.0 ** -23 * size).all()
+
+
+# ---- the most tokens --------------------------------------------------------------------
+def test_route_backward_of_the_most_tokens(ops):
+    """2^26 - 4 tokens of one choice: 2^32 - 256 threads."""
+    T = (1 << 26) - 4
+    ids = (torch.arange(T, device="cuda", dtype=torch.int32) & 1).view(T, 1)
+    w, grad = torch.full((T, 1), 0.5, device="cuda"), torch.arange(T, device="cuda").remainder(251).float().view(T, 1)
+    out = ops.moe_route_backward(ids, w, grad, 2)
+    want = torch.zeros(T, 2, device="cuda").scatter_(1, ids.long(), 0.25 * grad)  # w (g - w g): exact
+    assert torch.equal(out, want)
+    with pytest.raises(ops.MoEError):
+        grow = lambda t: torch.cat([t, t[:1]])  # noqa: E731
+        ops.moe_route_backward(grow(ids), grow(w), grow(grad), 2)

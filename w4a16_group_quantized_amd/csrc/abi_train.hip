@@ -251,8 +251,8 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_weights,
                        const float* grad_weights, int64_t T, int32_t E, int32_t top_k,
                        void* grad_logits, int32_t out_dtype, void* stream) {
   if (!dtype_ok(out_dtype) || T < 0 || E < 1 || top_k < 1) return MOE_ERR_INVALID_ARG;
-  // a wave per token, and 2^32 threads in a launch
-  if (E > kMaxExperts || top_k > kMaxTopK || T >= (1 << 26) || T * top_k > INT32_MAX)
+  // a wave per token, in workgroups of four, and less than 2^32 threads in a launch
+  if (E > kMaxExperts || top_k > kMaxTopK || T > (1 << 26) - 4 || T * top_k > INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!ok_ptr(topk_ids) || !ok_ptr(topk_weights) || !ok_ptr(grad_weights) || !ok_ptr(grad_logits))
