@@ -845,11 +845,11 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_weights,
  *   m = beta1 m + (1 - beta1) g;   v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay)
  *       - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
- * in fp32; p is rounded once to its type (and once to copy's), and is updated
- * from m and v before these are rounded to their states.  With eps 0 an element
- * whose v is 0 divides by 0; a positive eps may be as small as it likes (fp32
- * holds it as 2^-149 at least), and an element whose m and v are 0 then moves by
- * its weight decay alone.
+ * in fp32, beta and 1 - beta each rounded to it; p is rounded once to its type
+ * (and once to copy's), and is updated from m and v before these are rounded to
+ * their states.  With eps 0 an element whose v is 0 divides by 0.  A positive eps
+ * may be as small as it likes (fp32 holds it as 2^-149 at least): an element
+ * whose m and v are 0 then moves by its weight decay alone.
  *
  * States of 8 bits: elements in blocks of MOE_ADAMW_BLOCK (the last may be
  * short), per block one fp32 scale = largest magnitude / 1.875.  A code's
@@ -881,8 +881,8 @@ int moe_route_backward(const int32_t* topk_ids, const float* topk_weights,
  * repeats its step number, rate and seed when it is replayed.
  *
  * MOE_ERR_INVALID_ARG for state_bits, betas outside [0, 1), negative or
- * non-finite lr, eps or weight_decay, step < 1, buffers that overlap.  Limits:
- * n <= 2^33.
+ * non-finite lr, eps or weight_decay, lr weight_decay or lr / (1 - beta1^step)
+ * past fp32's range, step < 1, buffers that overlap.  Limits: n <= 2^33.
  */
 #define MOE_ADAMW_BLOCK 128
 typedef struct moe_adamw_tensor {

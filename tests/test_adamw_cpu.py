@@ -133,3 +133,13 @@ def test_moments_follow_only_with_another_noise_each_step(signed, beta, steps):
     # the nearest code is the same one again where (1 - beta) is under half of a sixteenth: nothing decays
     assert near == pytest.approx(beta ** -steps)
     assert abs(once - 1) > 2 * five
+
+
+# ---- scalars that fp32 does not hold -------------------------------------------------------
+@pytest.mark.parametrize("lr,beta1,decay,step", [(1e39, 0.9, 0.0, 1), (1e38, 0.9, 0.0, 1), (1e30, 1 - 1e-9, 0.0, 1),
+                                                 (1e20, 0.9, 1e19, 1000)])
+def test_adamw_refuses_rates_past_fp32(lr, beta1, decay, step):
+    """lr / (1 - beta1^step) or lr wd would be infinite, and NaN where it meets a zero."""
+    rows = [x for r in _table(1, 300, 32) for x in r.values()]
+    table = (ctypes.c_int64 * len(rows))(*rows)
+    assert ops.load_library().moe_adamw(table, 1, 32, lr, beta1, 0.999, 1e-8, decay, step, 0, None, None) == BAD

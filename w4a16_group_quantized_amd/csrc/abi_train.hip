@@ -299,6 +299,7 @@ int moe_adamw(const moe_adamw_tensor* tensors, int32_t count, int32_t state_bits
   s.rest2 = static_cast<float>(1 - beta2);
   s.decay = static_cast<float>(lr * weight_decay);
   s.size = static_cast<float>(lr / (1 - pow(beta1, static_cast<double>(step))));
+  if (isinf(s.decay) || isinf(s.size)) return MOE_ERR_INVALID_ARG;
   s.root = static_cast<float>(1 / sqrt(1 - pow(beta2, static_cast<double>(step))));
   // a positive eps stays positive: an element without moments moves by 0 / eps = 0
   s.eps = eps > 0 ? fmaxf(static_cast<float>(eps), 0x1p-149f) : 0.f;
