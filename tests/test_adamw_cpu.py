@@ -143,3 +143,12 @@ def test_adamw_refuses_rates_past_fp32(lr, beta1, decay, step):
     rows = [x for r in _table(1, 300, 32) for x in r.values()]
     table = (ctypes.c_int64 * len(rows))(*rows)
     assert ops.load_library().moe_adamw(table, 1, 32, lr, beta1, 0.999, 1e-8, decay, step, 0, None, None) == BAD
+
+
+@pytest.mark.parametrize("field,i,other,j", [("copy", 3, "m", 890), ("v", 899, "param", 0), ("grad", 899, "param", 0),
+                                             ("grad", 0, "copy", 899), ("param", 898, "copy", 899)])
+def test_adamw_refuses_overlaps_among_thousands_of_buffers(field, i, other, j):
+    for bits in (32, 8):
+        rows = _table(900, 1000, bits)
+        rows[j][other] = rows[i][field] + 996
+        assert _step(rows, bits) == BAD

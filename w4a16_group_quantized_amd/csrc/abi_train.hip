@@ -1,11 +1,10 @@
 // C ABI of the training operators: argument validation and dispatch.
 // Declarations and the full contract are in include/moe_w4a16.h.  Nothing here
-// allocates or frees device memory, or synchronises.
+// allocates, frees or synchronises.
 #include "train.h"
 #include "typed.h"
 
 #include <math.h>
-#include <stdlib.h>
 
 #include <algorithm>
 
@@ -80,61 +79,70 @@ int check_act(int32_t dtype, int64_t rows, int32_t I, const int32_t* offsets, in
   return rows * ((I + 7) / 8) >= (static_cast<int64_t>(1) << 32) - 256 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-// f(address, bytes) for each buffer that an AdamW step of a tensor writes.
+// f(address, bytes) for each buffer that an AdamW step writes.
 template <typename F>
-void adamw_written(const moe_adamw_tensor& t, int32_t state_bits, F&& f) {
-  const uint64_t n = static_cast<uint64_t>(t.n), blocks = (n + kAdamwBlock - 1) / kAdamwBlock;
+void adamw_written(const moe_adamw_tensor* tensors, int32_t count, int32_t state_bits, F&& f) {
   const auto put = [&](const void* p, uint64_t bytes) { f(reinterpret_cast<uint64_t>(p), bytes); };
-  put(t.param, n * dtype_bytes(t.param_dtype));
-  put(t.m, n * (state_bits / 8));
-  put(t.v, n * (state_bits / 8));
-  if (state_bits == 8) {
-    put(t.m_scales, blocks * sizeof(float));
-    put(t.v_scales, blocks * sizeof(float));
+  for (int32_t i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    const uint64_t n = static_cast<uint64_t>(t.n), blocks = (n + kAdamwBlock - 1) / kAdamwBlock;
+    put(t.param, n * dtype_bytes(t.param_dtype));
+    put(t.m, n * (state_bits / 8));
+    put(t.v, n * (state_bits / 8));
+    if (state_bits == 8) {
+      put(t.m_scales, blocks * sizeof(float));
+      put(t.v_scales, blocks * sizeof(float));
+    }
+    if (t.copy != nullptr) put(t.copy, n * dtype_bytes(t.copy_dtype));
   }
-  if (t.copy != nullptr) put(t.copy, n * dtype_bytes(t.copy_dtype));
 }
 
-// Whether a buffer that the step writes shares memory with any other of the call: ranges are
-// apart when their sorted beginnings and ends take turns.  Gradients and the scale of theirs
-// are only read, and may share theirs among them.  The ranges' place is the host's.
+// And for each that it only reads.
+template <typename F>
+void adamw_read(const moe_adamw_tensor* tensors, int32_t count, const float* grad_scale, F&& f) {
+  for (int32_t i = 0; i < count; ++i)
+    if (tensors[i].n > 0)
+      f(reinterpret_cast<uint64_t>(tensors[i].grad),
+        static_cast<uint64_t>(tensors[i].n) * dtype_bytes(tensors[i].grad_dtype));
+  if (grad_scale != nullptr) f(reinterpret_cast<uint64_t>(grad_scale), uint64_t{sizeof(float)});
+}
+
+// Whether every buffer that the step writes is apart from all others of the call.  Written
+// ranges are held kHeld at a time, on the stack: they are apart from each other when their
+// sorted beginnings and ends take turns, and then each of the rest is looked up among them.
 int check_apart(const moe_adamw_tensor* tensors, int32_t count, int32_t state_bits,
                 const float* grad_scale) {
-  constexpr size_t kNear = 512;  // 4 KB on the stack each: 170 tensors with states in fp32
-  uint64_t near_begins[kNear], near_ends[kNear];
-  size_t n = 0;
-  for (int32_t i = 0; i < count; ++i)
-    if (tensors[i].n > 0) adamw_written(tensors[i], state_bits, [&](uint64_t, uint64_t) { ++n; });
-  uint64_t* far = nullptr;
-  if (n > kNear) {
-    far = static_cast<uint64_t*>(malloc(2 * n * sizeof(uint64_t)));
-    if (far == nullptr) return MOE_ERR_UNSUPPORTED;
-  }
-  uint64_t* begins = far != nullptr ? far : near_begins;
-  uint64_t* ends = far != nullptr ? far + n : near_ends;
-  size_t at = 0;
-  for (int32_t i = 0; i < count; ++i)
-    if (tensors[i].n > 0)
-      adamw_written(tensors[i], state_bits, [&](uint64_t p, uint64_t bytes) {
-        begins[at] = p;
-        ends[at++] = p + bytes;
+  constexpr size_t kHeld = 2048;  // 32 KB; 340 tensors with 8-bit states and copies
+  uint64_t begins[kHeld], ends[kHeld];
+  for (size_t first = 0, all = 1; first < all; first += kHeld) {
+    size_t n = 0;
+    all = 0;
+    adamw_written(tensors, count, state_bits, [&](uint64_t from, uint64_t bytes) {
+      if (all >= first && n < kHeld) {
+        begins[n] = from;
+        ends[n++] = from + bytes;
+      }
+      ++all;
+    });
+    std::sort(begins, begins + n);
+    std::sort(ends, ends + n);
+    bool apart = true;
+    for (size_t i = 1; i < n; ++i) apart = apart && ends[i - 1] <= begins[i];
+    if (!apart) return MOE_ERR_INVALID_ARG;
+    const auto look_up = [&](uint64_t from, uint64_t bytes) {
+      const size_t next = std::upper_bound(ends, ends + n, from) - ends;
+      apart = apart && (next == n || from + bytes <= begins[next]);
+    };
+    size_t at = 0;
+    if (first + n < all)
+      adamw_written(tensors, count, state_bits, [&](uint64_t from, uint64_t bytes) {
+        if (at++ >= first + n) look_up(from, bytes);
       });
-  std::sort(begins, begins + n);
-  std::sort(ends, ends + n);
-  bool apart = true;
-  for (size_t i = 1; i < n; ++i) apart = apart && ends[i - 1] <= begins[i];
-  // a range that is only read: the first written one that ends behind its beginning
-  const auto clear = [&](const void* p, uint64_t bytes) {
-    const uint64_t from = reinterpret_cast<uint64_t>(p);
-    const size_t next = std::upper_bound(ends, ends + n, from) - ends;
-    return next == n || from + bytes <= begins[next];
-  };
-  for (int32_t i = 0; apart && i < count; ++i)
-    if (tensors[i].n > 0)
-      apart = clear(tensors[i].grad, static_cast<uint64_t>(tensors[i].n) * dtype_bytes(tensors[i].grad_dtype));
-  if (apart && grad_scale != nullptr) apart = clear(grad_scale, sizeof(float));
-  free(far);
-  return apart ? MOE_OK : MOE_ERR_INVALID_ARG;
+    adamw_read(tensors, count, grad_scale, look_up);
+    if (!apart) return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
 }
 
 }  // namespace
