@@ -767,7 +767,8 @@ int moe_combine_backward(const void* grad_out, int32_t grad_dtype,
  *                   time must not share it.
  *
  * Any N, K and strides; where N, K, the strides and the addresses of a and grad
- * are multiples of 8 elements the calls are about twice as fast.  An output must not overlap an input.  rows == 0 is valid;
+ * are multiples of 8 elements the calls are 1.5 to 2 times as fast.  An output
+ * must not overlap an input.  rows == 0 is valid;
  * moe_grouped_gemm_backward_weights then still writes grad_w.
  *
  * Limits: fp32 operands are MOE_ERR_UNSUPPORTED; 1 <= E <= 4096; 1 <= N, K <=

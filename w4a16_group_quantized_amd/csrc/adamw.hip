@@ -3,10 +3,10 @@
 //   p = p (1 - lr wd) - (lr / c1) m / (sqrt(v) / sqrt(c2) + eps),   c = 1 - b^step
 // with m and v in fp32, or in 8 bits per element and one fp32 scale per block of
 // 128.  Bound by memory: each value is read once and written once.  105 million
-// elements: fp32 parameters and gradients and a bf16 copy, 8-bit states 324 us (5.8
-// TB/s), fp32 states 570 (5.5); bf16 parameters and gradients, no copy, 415 us with
-// fp32 states (5.6) and 231 with 8-bit ones (4.6: the noise's three multiplications
-// an element are as long as its 10 bytes).  30 tensors of 2560 elements, one launch: 5 us.
+// elements: fp32 parameters and gradients and a bf16 copy, 8-bit states 324 to 345 us
+// (5.5 to 5.8 TB/s), fp32 states 570 (5.5); bf16 parameters and gradients, no copy, 415
+// us with fp32 states (5.6) and 195 to 231 with 8-bit ones (4.6 to 5.4: the noise's three
+// multiplications an element are as long as its 10 bytes).  30 tensors of 2560 elements, one launch: 5 us.
 //
 // 8-bit states.  A block's scale is its largest magnitude / 1.875.  m has a sign,
 // 4 exponent and 3 mantissa bits, v, which is not negative, 5 and 3: code c stands

